@@ -1,0 +1,225 @@
+// dense_api.cuh -- host side of the dense attention calls (part of sla_api.cu's
+// translation unit): validation, workspace, launches.
+#pragma once
+
+namespace {
+
+int dense_es(const sla_dense_params_t*) { return 2; }   // both I/O types have 16 bits
+
+sla_status_t dense_check(const sla_dense_params_t* p) {
+    if (!p) return SLA_ERR_INVALID_ARG;
+    if (p->B <= 0 || p->H <= 0 || p->Hk <= 0 || p->Nq <= 0 || p->Nk < 0 || p->P < 0 || p->d <= 0)
+        return SLA_ERR_INVALID_ARG;
+    if (p->H % p->Hk != 0) return SLA_ERR_INVALID_ARG;
+    if (p->io_dtype != SLA_IO_BF16 && p->io_dtype != SLA_IO_FP16) return SLA_ERR_INVALID_ARG;
+    if ((p->causal != 0 && p->causal != 1) || (p->differential != 0 && p->differential != 1))
+        return SLA_ERR_INVALID_ARG;
+    if (!std::isfinite(p->sm_scale)) return SLA_ERR_INVALID_ARG;
+    if (p->d != 64 && p->d != 128) return SLA_ERR_UNSUPPORTED;
+    if (p->B > 65535 || p->H > 65535) return SLA_ERR_UNSUPPORTED;
+    if (static_cast<long long>(p->B) * p->H > (1LL << 30) / p->Nq) return SLA_ERR_UNSUPPORTED;
+    if (static_cast<long long>(p->Nk) + p->P >= (1LL << 30)) return SLA_ERR_UNSUPPORTED;
+    return SLA_OK;
+}
+
+// A tensor's strides, checked: `st` has nd (2: head, token; 3: batch, head, token)
+// values, NULL for a dense tensor.  A dimension of one entry gets stride 0.
+sla_status_t dense_strides(const int64_t* st, int nd, int B, int H, int N, int d, bool output, sla::DenseT& t) {
+    const long long size[3] = {nd == 3 ? B : 1, H, N};
+    long long s[3] = {static_cast<long long>(H) * N * d, static_cast<long long>(N) * d, d};
+    if (st)
+        for (int x = 0; x < nd; ++x) s[3 - nd + x] = st[x];
+    for (int x = 0; x < 3; ++x) {
+        if (size[x] <= 1) { s[x] = 0; continue; }
+        if (s[x] < 0 || s[x] % 8 != 0 || s[x] >= (1LL << 36)) return SLA_ERR_INVALID_ARG;
+        if (s[x] == 0 && (output || x == 2)) return SLA_ERR_INVALID_ARG;
+    }
+    if (output) {      // entries apart: in the order of the strides, each at least the extent below it
+        int o[3] = {0, 1, 2};
+        std::sort(o, o + 3, [&](int x, int y) { return s[x] < s[y]; });
+        long long extent = d;
+        for (int x : o) {
+            if (size[x] <= 1) continue;
+            if (s[x] < extent) return SLA_ERR_INVALID_ARG;
+            extent += s[x] * (size[x] - 1);
+        }
+    }
+    t = {s[0], s[1], s[2]};
+    return SLA_OK;
+}
+
+struct DenseWs {
+    size_t delta, total;
+};
+
+DenseWs dense_layout(const sla_dense_params_t* p) {
+    DenseWs w{};
+    size_t off = 0;
+    auto take = [&](size_t bytes) { size_t o = off; off = align_up(off + bytes); return o; };
+    w.delta = take(2ull * p->B * p->H * p->Nq * 4);
+    w.total = off;
+    return w;
+}
+
+sla_status_t dense_check_ws(const sla_dense_params_t* p, void* ws, size_t ws_bytes, DenseWs& w) {
+    w = dense_layout(p);
+    if (!ws || !aligned(ws, kAlign) || ws_bytes < w.total) return SLA_ERR_WORKSPACE;
+    return SLA_OK;
+}
+
+void dense_fill(const sla_dense_params_t* p, sla::DenseArgs& a) {
+    a.B = p->B, a.H = p->H, a.Hk = p->Hk, a.G = p->H / p->Hk;
+    a.Nq = p->Nq, a.Nk = p->Nk, a.P = p->P;
+    a.causal = p->causal;
+    const double tau = p->sm_scale > 0.f ? static_cast<double>(p->sm_scale)
+                                         : 1.0 / std::sqrt(static_cast<double>(p->differential ? p->d / 2 : p->d));
+    a.scale = static_cast<float>(tau);
+    a.scale_log2 = static_cast<float>(tau * 1.4426950408889634);
+}
+
+// lambda, lengths and lse: small arrays without strides.
+sla_status_t dense_small(const sla_dense_params_t* p, const void* lambda, const int32_t* q_len, const int32_t* kv_len,
+                         const float* lse) {
+    if (p->differential ? !lambda || !aligned(lambda, 2) : lambda != nullptr) return SLA_ERR_INVALID_ARG;
+    if (!aligned(q_len, 4) || !aligned(kv_len, 4) || !aligned(lse, 4)) return SLA_ERR_INVALID_ARG;
+    return SLA_OK;
+}
+
+template <int D, typename T>
+sla_status_t dense_fwd(const sla_dense_params_t* p, const sla::DenseArgs& a, cudaStream_t st) {
+    const long long rows = static_cast<long long>(p->B) * p->H * p->Nq;
+    const unsigned grid = static_cast<unsigned>((rows + 3) / 4);
+    Span sp(SLA_KERNEL_DENSE, st);
+    if (p->differential)
+        sla::dense_fwd_rows_kernel<D, T, true><<<grid, 128, 0, st>>>(a);
+    else
+        sla::dense_fwd_rows_kernel<D, T, false><<<grid, 128, 0, st>>>(a);
+    return launch_status();
+}
+
+template <int D, typename T>
+sla_status_t dense_bwd(const sla_dense_params_t* p, const sla::DenseArgs& a, cudaStream_t st) {
+    const long long rows = static_cast<long long>(p->B) * p->H * p->Nq,
+                    keys = static_cast<long long>(p->B) * p->Hk * p->Nk;
+    {
+        Span sp(SLA_KERNEL_DENSE_BWD, st);
+        sla::dense_delta_kernel<D, T><<<static_cast<unsigned>((rows + 3) / 4), 128, 0, st>>>(a);
+    }
+    {
+        Span sp(SLA_KERNEL_DENSE_BWD, st);
+        sla::dense_dlambda_kernel<T><<<p->H, 256, 0, st>>>(a);
+    }
+    {
+        Span sp(SLA_KERNEL_DENSE_BWD, st);
+        sla::dense_bwd_rows_kernel<D, T, false><<<static_cast<unsigned>((rows + 3) / 4), 128, 0, st>>>(a);
+    }
+    if (keys) {
+        Span sp(SLA_KERNEL_DENSE_BWD, st);
+        sla::dense_bwd_rows_kernel<D, T, true><<<static_cast<unsigned>((keys + 3) / 4), 128, 0, st>>>(a);
+    }
+    return launch_status();
+}
+
+template <typename F>
+sla_status_t dense_dispatch(const sla_dense_params_t* p, F f) {
+    if (p->io_dtype == SLA_IO_BF16)
+        return p->d == 128 ? f(std::integral_constant<int, 128>{}, __nv_bfloat16{})
+                           : f(std::integral_constant<int, 64>{}, __nv_bfloat16{});
+    return p->d == 128 ? f(std::integral_constant<int, 128>{}, __half{})
+                       : f(std::integral_constant<int, 64>{}, __half{});
+}
+
+}  // namespace
+
+extern "C" size_t sla_dense_workspace_size(const sla_dense_params_t* p) {
+    if (dense_check(p) != SLA_OK) return 0;
+    return dense_layout(p).total;
+}
+
+extern "C" sla_status_t sla_diff_forward(const sla_dense_params_t* p, const int64_t* strides, const void* q,
+                                         const void* k, const void* v, const void* lambda, const int32_t* q_len,
+                                         const int32_t* kv_len, void* out, void* out2, float* lse, void* workspace,
+                                         size_t ws_bytes, sla_stream_t stream) {
+    sla_status_t s = dense_check(p);
+    if (s != SLA_OK) return s;
+    if (p->differential != 1 || p->P != 0) return SLA_ERR_INVALID_ARG;
+    if ((s = check_tensor(q, 16)) || (s = check_tensor(out, 16)) || (p->Nk && (s = check_tensor(k, 16))) ||
+        (p->Nk && (s = check_tensor(v, 16))) || (s = dense_small(p, lambda, q_len, kv_len, lse)))
+        return s;
+    if (!aligned(out2, 16)) return SLA_ERR_INVALID_ARG;
+    sla::DenseArgs a{};
+    if ((s = dense_strides(strides, 3, p->B, p->H, p->Nq, p->d, false, a.qs)) ||
+        (s = dense_strides(strides ? strides + 3 : nullptr, 3, p->B, p->Hk, p->Nk, p->d, false, a.ks)) ||
+        (s = dense_strides(strides ? strides + 6 : nullptr, 3, p->B, p->Hk, p->Nk, p->d, false, a.vs)) ||
+        (s = dense_strides(strides ? strides + 9 : nullptr, 3, p->B, p->H, p->Nq, p->d, true, a.os)))
+        return s;
+    DenseWs w;
+    if ((s = dense_check_ws(p, workspace, ws_bytes, w))) return s;
+    dense_fill(p, a);
+    a.q = q, a.k = k, a.v = v, a.lam = lambda, a.q_len = q_len, a.kv_len = kv_len;
+    a.out = out, a.out2 = out2, a.lse = lse;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return finish(dense_dispatch(p, [&](auto d, auto t) { return dense_fwd<d(), decltype(t)>(p, a, st); }), st);
+}
+
+extern "C" sla_status_t sla_diff_backward(const sla_dense_params_t* p, const int64_t* strides, const void* q,
+                                          const void* k, const void* v, const void* lambda, const int32_t* q_len,
+                                          const int32_t* kv_len, const void* out, const void* out2, const float* lse,
+                                          const void* dout, void* dq, void* dk, void* dv, void* dlambda,
+                                          void* workspace, size_t ws_bytes, sla_stream_t stream) {
+    sla_status_t s = dense_check(p);
+    if (s != SLA_OK) return s;
+    if (p->differential != 1 || p->P != 0) return SLA_ERR_INVALID_ARG;
+    if ((s = check_tensor(q, 16)) || (s = check_tensor(out, 16)) || (s = check_tensor(out2, 16)) ||
+        (s = check_tensor(lse, 4)) || (s = check_tensor(dout, 16)) || (s = check_tensor(dq, 16)) ||
+        (s = check_tensor(dlambda, 2)) || (s = dense_small(p, lambda, q_len, kv_len, lse)))
+        return s;
+    if (p->Nk && ((s = check_tensor(k, 16)) || (s = check_tensor(v, 16)) || (s = check_tensor(dk, 16)) ||
+                  (s = check_tensor(dv, 16))))
+        return s;
+    sla::DenseArgs a{};
+    struct { sla::DenseT* t; int h, n; bool output; } const want[8] = {
+        {&a.qs, p->H, p->Nq, false}, {&a.ks, p->Hk, p->Nk, false}, {&a.vs, p->Hk, p->Nk, false},
+        {&a.os, p->H, p->Nq, false}, {&a.dos, p->H, p->Nq, false}, {&a.dqs, p->H, p->Nq, true},
+        {&a.dks, p->Hk, p->Nk, true}, {&a.dvs, p->Hk, p->Nk, true}};
+    for (int x = 0; x < 8; ++x)
+        if ((s = dense_strides(strides ? strides + 3 * x : nullptr, 3, p->B, want[x].h, want[x].n, p->d,
+                               want[x].output, *want[x].t)))
+            return s;
+    DenseWs w;
+    if ((s = dense_check_ws(p, workspace, ws_bytes, w))) return s;
+    dense_fill(p, a);
+    a.q = q, a.k = k, a.v = v, a.lam = lambda, a.q_len = q_len, a.kv_len = kv_len;
+    a.out = const_cast<void*>(out), a.out2 = const_cast<void*>(out2), a.lse = const_cast<float*>(lse);
+    a.dout = dout, a.dq = dq, a.dk = dk, a.dv = dv, a.dlam = dlambda;
+    a.delta = at<float>(workspace, w.delta);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return finish(dense_dispatch(p, [&](auto d, auto t) { return dense_bwd<d(), decltype(t)>(p, a, st); }), st);
+}
+
+extern "C" sla_status_t sla_prefix_forward(const sla_dense_params_t* p, const int64_t* strides, const void* q,
+                                           const void* k_prefix, const void* v_prefix, const void* k, const void* v,
+                                           const void* lambda, const int32_t* q_len, const int32_t* kv_len, void* out,
+                                           float* lse, void* workspace, size_t ws_bytes, sla_stream_t stream) {
+    sla_status_t s = dense_check(p);
+    if (s != SLA_OK) return s;
+    if ((s = check_tensor(q, 16)) || (s = check_tensor(out, 16)) || (s = dense_small(p, lambda, q_len, kv_len, lse)))
+        return s;
+    if (p->Nk && ((s = check_tensor(k, 16)) || (s = check_tensor(v, 16)))) return s;
+    if (p->P && ((s = check_tensor(k_prefix, 16)) || (s = check_tensor(v_prefix, 16)))) return s;
+    sla::DenseArgs a{};
+    if ((s = dense_strides(strides, 3, p->B, p->H, p->Nq, p->d, false, a.qs)) ||
+        (s = dense_strides(strides ? strides + 3 : nullptr, 2, 1, p->Hk, p->P, p->d, false, a.kps)) ||
+        (s = dense_strides(strides ? strides + 5 : nullptr, 2, 1, p->Hk, p->P, p->d, false, a.vps)) ||
+        (s = dense_strides(strides ? strides + 7 : nullptr, 3, p->B, p->Hk, p->Nk, p->d, false, a.ks)) ||
+        (s = dense_strides(strides ? strides + 10 : nullptr, 3, p->B, p->Hk, p->Nk, p->d, false, a.vs)) ||
+        (s = dense_strides(strides ? strides + 13 : nullptr, 3, p->B, p->H, p->Nq, p->d, true, a.os)))
+        return s;
+    DenseWs w;
+    if ((s = dense_check_ws(p, workspace, ws_bytes, w))) return s;
+    dense_fill(p, a);
+    a.q = q, a.k = k, a.v = v, a.kp = k_prefix, a.vp = v_prefix, a.lam = lambda;
+    a.q_len = q_len, a.kv_len = kv_len, a.out = out, a.lse = lse;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return finish(dense_dispatch(p, [&](auto d, auto t) { return dense_fwd<d(), decltype(t)>(p, a, st); }), st);
+}

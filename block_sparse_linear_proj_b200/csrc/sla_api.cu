@@ -5,10 +5,12 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdlib>
 #include <cstring>
 #include <mutex>
+#include <type_traits>
 #include <vector>
 
 #include "../../include/sla.h"
@@ -16,6 +18,7 @@
 #include "cocluster.cuh"
 #include "common.cuh"
 #include "cov.cuh"
+#include "dense.cuh"
 #include "kv_stats.cuh"
 #include "router.cuh"
 
@@ -1180,3 +1183,5 @@ extern "C" sla_status_t sla_route_noalloc(const sla_params_t* p, const void* q, 
     if ((s = route_scratch_ptr(st, &scratch))) return s;
     return finish(run_router(p, q, k, w_q, w_k, lut, scratch, w, st), st);
 }
+
+#include "dense_api.cuh"

@@ -36,14 +36,17 @@ SLA_LUT_COMPUTE = 0
 SLA_LUT_GIVEN = 1
 SLA_OUT_BF16 = 0
 SLA_OUT_FP32 = 1
+SLA_IO_BF16 = 0
+SLA_IO_FP16 = 1
 
 EXPORTED = ("sla_workspace_size", "sla_route", "sla_forward", "sla_pisa_forward",
             "sla_status_string", "sla_check_device_status", "sla_version",
             "sla_profile_enable", "sla_profile_read", "sla_route_noalloc",
             "sla_cocluster", "sla_cocluster_workspace_size", "sla_permute_rows",
-            "sla_forward_host", "sla_pisa_forward_host")
+            "sla_forward_host", "sla_pisa_forward_host", "sla_dense_workspace_size",
+            "sla_diff_forward", "sla_diff_backward", "sla_prefix_forward")
 KERNEL_KINDS = ("pool", "kv_stats", "h_reduce", "fold_w", "score_topk", "attn", "quant_q", "project",
-                "cov", "pre_attn", "cocluster", "permute")
+                "cov", "pre_attn", "cocluster", "permute", "dense", "dense_bwd")
 # profile entries that are phases of a call, not kernel launches
 PHASE_KINDS = ("pre_attn",)
 
@@ -55,6 +58,13 @@ class SlaParams(ctypes.Structure):
                 ("sparse_dtype", ctypes.c_int32), ("lut_mode", ctypes.c_int32),
                 ("out_dtype", ctypes.c_int32), ("pisa_first_order", ctypes.c_int32),
                 ("pisa_cov_lambda", ctypes.c_float)]
+
+
+class SlaDenseParams(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("H", ctypes.c_int32), ("Hk", ctypes.c_int32),
+                ("Nq", ctypes.c_int32), ("Nk", ctypes.c_int32), ("P", ctypes.c_int32),
+                ("d", ctypes.c_int32), ("sm_scale", ctypes.c_float), ("io_dtype", ctypes.c_int32),
+                ("causal", ctypes.c_int32), ("differential", ctypes.c_int32)]
 
 
 class SlaError(RuntimeError):
@@ -112,6 +122,15 @@ def load():
             lib.sla_pisa_forward_host.argtypes = [PP, P, P, P, P, P, P, P, P, P, P, P, ctypes.c_int32, P,
                                                   ctypes.c_size_t, P]
             lib.sla_pisa_forward_host.restype = ctypes.c_int
+            PD = ctypes.POINTER(SlaDenseParams)
+            lib.sla_dense_workspace_size.argtypes = [PD]
+            lib.sla_dense_workspace_size.restype = ctypes.c_size_t
+            lib.sla_diff_forward.argtypes = [PD] + [P] * 10 + [P, ctypes.c_size_t, P]
+            lib.sla_diff_forward.restype = ctypes.c_int
+            lib.sla_diff_backward.argtypes = [PD] + [P] * 15 + [P, ctypes.c_size_t, P]
+            lib.sla_diff_backward.restype = ctypes.c_int
+            lib.sla_prefix_forward.argtypes = [PD] + [P] * 11 + [P, ctypes.c_size_t, P]
+            lib.sla_prefix_forward.restype = ctypes.c_int
             _lib = lib
     return _lib
 
@@ -376,4 +395,123 @@ def sla_forward_coclustered(p, q, k, v, alpha, w_q, w_k, q_perm, k_perm, lut, ou
     sla_forward(p, scratch["q"], scratch["k"], scratch["v"], scratch["alpha"], w_q, w_k, lut, scratch["out"], ws,
                 stream)
     sla_permute_rows(scratch["out"], q_perm, out, inverse=True, stream=stream)
+    return out
+
+
+# ------------------------------------------------------------------ dense attention
+def dense_params(B, H, Hk, Nq, Nk, d, prefix=0, sm_scale=0.0, io_dtype=SLA_IO_BF16, causal=False,
+                 differential=False) -> SlaDenseParams:
+    return SlaDenseParams(B, H, Hk, Nq, Nk, prefix, d, float(sm_scale), io_dtype, 1 if causal else 0,
+                          1 if differential else 0)
+
+
+def io_torch_dtype(p: SlaDenseParams):
+    return torch.float16 if p.io_dtype == SLA_IO_FP16 else torch.bfloat16
+
+
+def dense_workspace(p: SlaDenseParams, device=None) -> torch.Tensor:
+    """A workspace tensor for sla_diff_forward, sla_diff_backward and
+    sla_prefix_forward with these parameters."""
+    n = int(load().sla_dense_workspace_size(ctypes.byref(p)))
+    if n == 0:
+        raise SlaError(SLA_ERR_INVALID_ARG, "sla_dense_workspace_size")
+    return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+
+
+class _DenseArgs:
+    """Addresses and strides of one dense call's tensors, checked."""
+
+    def __init__(self, p):
+        self.dtype, self.dev, self.strides = io_torch_dtype(p), torch.cuda.current_device(), []
+
+    def _addr(self, t, dtype, shape, name):
+        if t.dtype != dtype:
+            raise TypeError("%s: expected %s, got %s" % (name, dtype, t.dtype))
+        if t.shape != shape:
+            raise ValueError("%s: expected shape %s, got %s" % (name, shape, tuple(t.shape)))
+        if t.numel() == 0:
+            return None
+        if t.get_device() != self.dev:     # -1 for a host tensor
+            raise ValueError("%s is on %s but the current device is cuda:%d" % (name, t.device, self.dev))
+        return t.data_ptr()
+
+    def strided(self, t, shape, name):
+        """Any strides with a dense last dimension; None stands for an empty tensor."""
+        n = len(shape) - 1
+        if t is None:
+            if 0 not in shape:
+                raise ValueError("%s is missing" % name)
+            self.strides += [0] * n
+            return None
+        a = self._addr(t, self.dtype, shape, name)
+        st = t.stride()
+        if st[n] != 1 and a is not None:
+            raise ValueError("%s: the last dimension must be dense" % name)
+        self.strides += st[:n]
+        return a
+
+    def dense(self, t, dtype, shape, name):
+        if t is None:
+            return None
+        a = self._addr(t, dtype, shape, name)
+        if not t.is_contiguous():
+            raise ValueError("%s must be contiguous" % name)
+        return a
+
+    def array(self):
+        return (ctypes.c_int64 * len(self.strides))(*self.strides)
+
+
+def _lse_shape(p):
+    return (p.B, p.H, 2, p.Nq) if p.differential else (p.B, p.H, p.Nq)
+
+
+def sla_diff_forward(p, q, k, v, lam, out, ws, lse=None, out2=None, q_len=None, kv_len=None, stream=None):
+    """Differential attention into ``out``: softmax over the first halves of q and
+    k times v, minus ``lam`` [H] times the same over the second halves.  q, out
+    [B,H,Nq,d], k, v [B,Hk,Nk,d], any batch, head and token strides.  ``lse``
+    (fp32 [B,H,2,Nq]) and ``out2`` ([B,H,Nq,d]) are written for the backward call."""
+    qs, ks = (p.B, p.H, p.Nq, p.d), (p.B, p.Hk, p.Nk, p.d)
+    a = _DenseArgs(p)
+    args = [a.strided(q, qs, "q"), a.strided(k, ks, "k"), a.strided(v, ks, "v"),
+            a.dense(lam, a.dtype, (p.H,), "lam"), a.dense(q_len, torch.int32, (p.B,), "q_len"),
+            a.dense(kv_len, torch.int32, (p.B,), "kv_len"), a.strided(out, qs, "out"),
+            a.dense(out2, a.dtype, qs, "out2"), a.dense(lse, torch.float32, _lse_shape(p), "lse")]
+    rc = load().sla_diff_forward(ctypes.byref(p), a.array(), *args, _ptr(ws), _nbytes(ws), _stream(stream))
+    _raise(rc, "sla_diff_forward")
+    return out
+
+
+def sla_diff_backward(p, q, k, v, lam, out, out2, lse, dout, dq, dk, dv, dlam, ws, q_len=None, kv_len=None,
+                      stream=None):
+    """Gradients of sla_diff_forward for ``dout`` into dq, dk, dv and ``dlam`` [H];
+    out, out2 and lse are the forward call's."""
+    qs, ks = (p.B, p.H, p.Nq, p.d), (p.B, p.Hk, p.Nk, p.d)
+    a = _DenseArgs(p)
+    tq, tk, tv = a.strided(q, qs, "q"), a.strided(k, ks, "k"), a.strided(v, ks, "v")
+    to, tdo = a.strided(out, qs, "out"), a.strided(dout, qs, "dout")
+    tdq, tdk, tdv = a.strided(dq, qs, "dq"), a.strided(dk, ks, "dk"), a.strided(dv, ks, "dv")
+    rc = load().sla_diff_backward(
+        ctypes.byref(p), a.array(), tq, tk, tv, a.dense(lam, a.dtype, (p.H,), "lam"),
+        a.dense(q_len, torch.int32, (p.B,), "q_len"), a.dense(kv_len, torch.int32, (p.B,), "kv_len"), to,
+        a.dense(out2, a.dtype, qs, "out2"), a.dense(lse, torch.float32, _lse_shape(p), "lse"), tdo, tdq, tdk, tdv,
+        a.dense(dlam, a.dtype, (p.H,), "dlam"), _ptr(ws), _nbytes(ws), _stream(stream))
+    _raise(rc, "sla_diff_backward")
+    return dq, dk, dv, dlam
+
+
+def sla_prefix_forward(p, q, k_prefix, v_prefix, k, v, out, ws, lam=None, lse=None, q_len=None, kv_len=None,
+                       stream=None):
+    """Attention of B sequences over p.P shared prefix keys (k_prefix, v_prefix
+    [Hk,P,d]) and their own keys (k, v [B,Hk,Nk,d]) into ``out`` [B,H,Nq,d]; with
+    p.differential the difference of two maps, weighed by ``lam`` [H].  ``lse``:
+    fp32 [B,H,Nq], differential [B,H,2,Nq]."""
+    qs, ks, kps = (p.B, p.H, p.Nq, p.d), (p.B, p.Hk, p.Nk, p.d), (p.Hk, p.P, p.d)
+    a = _DenseArgs(p)
+    args = [a.strided(q, qs, "q"), a.strided(k_prefix, kps, "k_prefix"), a.strided(v_prefix, kps, "v_prefix"),
+            a.strided(k, ks, "k"), a.strided(v, ks, "v"), a.dense(lam, a.dtype, (p.H,), "lam"),
+            a.dense(q_len, torch.int32, (p.B,), "q_len"), a.dense(kv_len, torch.int32, (p.B,), "kv_len"),
+            a.strided(out, qs, "out"), a.dense(lse, torch.float32, _lse_shape(p), "lse")]
+    rc = load().sla_prefix_forward(ctypes.byref(p), a.array(), *args, _ptr(ws), _nbytes(ws), _stream(stream))
+    _raise(rc, "sla_prefix_forward")
     return out

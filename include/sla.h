@@ -296,6 +296,112 @@ sla_status_t sla_cocluster(const sla_params_t *p, const void *q, const void *k,
 sla_status_t sla_permute_rows(const void *src, const int32_t *perm, void *dst, int64_t BH,
                               int32_t N, int32_t row_bytes, int32_t inverse, sla_stream_t stream);
 
+/*
+ * Dense attention: differential attention (with its gradients) and attention
+ * for a batch that shares a prefix.
+ *
+ * Shapes: H query heads share Hk key/value heads, H % Hk == 0, query head h
+ * reading key/value head h / (H / Hk).  B sequences of Nq queries and Nk own
+ * keys; P prefix keys that every sequence sees before its own ones
+ * (sla_prefix_forward).  d in {64, 128}.  Any Nq >= 1 and any Nk, P >= 0 with
+ * B * H * Nq and Nk + P below 2^30 are taken (B, H at most 65535).
+ *   q, out        : [B, H, Nq, d]       k, v              : [B, Hk, Nk, d]
+ *   out2          : [B, H, Nq, d]       k_prefix, v_prefix: [Hk, P, d]
+ *   lse           : fp32 [B, H, Nq], differential [B, H, 2, Nq]
+ *   lambda        : [H]
+ *   q_len, kv_len : int32 [B], or NULL for Nq and Nk everywhere
+ * Tensors are of the type io_dtype selects except lse and the lengths.
+ * `strides` gives, in elements, the batch, head and token strides of the
+ * tensors a call names for it (k_prefix and v_prefix: head and token), the
+ * last dimension always being dense; NULL means dense row-major tensors.  The
+ * stride of a dimension of one entry is not read.  The others are multiples of
+ * 8 elements; a batch or head stride of an input may be 0 (a broadcast input:
+ * its gradient is per entry, the caller sums it); entries of an output must
+ * not overlap.  out2 and lse are always dense.  Pointers are aligned to 16
+ * bytes; lambda and dlambda to 2; lse and the lengths to 4.
+ *
+ * Masks.  Own keys from kv_len[b] on are padding, and so are queries from
+ * q_len[b] on; padding is never read into a result, whatever it holds.  With
+ * causal = 1 the q_len[b] queries are the last q_len[b] of the kv_len[b] own
+ * keys: query i sees own key j if j <= i + kv_len[b] - q_len[b].  The prefix is
+ * seen by every query.  A query that sees no key, or is padding, gets out = 0,
+ * out2 = 0, lse = -inf and dq = 0; a key that no query sees gets dk = dv = 0,
+ * padding included.  A length below 0 or above Nq (Nk) is taken as 0 or Nq (Nk)
+ * and flagged SLA_ERR_DEVICE_CHECK.
+ *
+ * Numerics: products on the tensor cores with fp32 accumulation; softmax
+ * statistics, lse and every sum in fp32; the softmax weights and their
+ * gradients enter their products in io_dtype.  Results do not depend on how
+ * the GPU orders its work: equal calls give equal bits.
+ */
+typedef enum { SLA_IO_BF16 = 0, SLA_IO_FP16 = 1 } sla_io_dtype_t;
+
+typedef struct sla_dense_params {
+    int32_t B, H, Hk;        /* sequences, query heads, key/value heads           */
+    int32_t Nq, Nk;          /* queries and own keys a sequence has room for      */
+    int32_t P;               /* shared prefix keys                                */
+    int32_t d;               /* head dim                                          */
+    float sm_scale;          /* softmax scale tau; <= 0 means 1/sqrt(d), and
+                                1/sqrt(d/2) for the two maps of differential = 1  */
+    int32_t io_dtype;        /* sla_io_dtype_t                                    */
+    int32_t causal;          /* 1: causal mask over the own keys                  */
+    int32_t differential;    /* 1: differential attention                         */
+} sla_dense_params_t;
+
+/* Bytes of device workspace (256-byte aligned) that the three calls below need
+ * for these parameters, the maximum over them; 0 if the parameters are invalid. */
+size_t sla_dense_workspace_size(const sla_dense_params_t *p);
+
+/*
+ * sla_diff_forward -- differential attention.  Each head's d dimensions of q
+ * and k are two halves, q = [q1 | q2] and k = [k1 | k2], with a softmax map each:
+ *   O_m = softmax(tau q_m k_m^T) v,   out = O_1 - lambda_h O_2.
+ * Needs p->differential = 1 and p->P = 0.  out2 (the second map's O_2) and lse
+ * (each map's log-sum-exp, natural logarithm) are written if not NULL; the
+ * backward call reads both.  strides: 12 values, of q, k, v, out.
+ * Few queries against many keys (single tokens against a cache) are split over
+ * the keys and joined.
+ */
+sla_status_t sla_diff_forward(const sla_dense_params_t *p, const int64_t *strides, const void *q,
+                              const void *k, const void *v, const void *lambda,
+                              const int32_t *q_len, const int32_t *kv_len, void *out, void *out2,
+                              float *lse, void *workspace, size_t ws_bytes, sla_stream_t stream);
+
+/*
+ * sla_diff_backward -- the gradients of sla_diff_forward for dout, from its
+ * inputs and its out, out2 and lse.  With P_m the softmax maps, dP = dout v^T and
+ * delta_m = rowsum(dout (.) O_m):
+ *   dv = (P_1 - lambda P_2)^T dout
+ *   dS_1 = tau P_1 (.) (dP - delta_1),  dS_2 = -lambda tau P_2 (.) (dP - delta_2)
+ *   dq_m = dS_m k_m,  dk_m = dS_m^T q_m,  dlambda_h = -sum delta_2
+ * dk and dv are summed over the query heads that share a key/value head, and
+ * dlambda over batch and queries.  Rows of dout at padding queries are not read.
+ * strides: 24 values, of q, k, v, out, dout, dq, dk, dv.
+ */
+sla_status_t sla_diff_backward(const sla_dense_params_t *p, const int64_t *strides, const void *q,
+                               const void *k, const void *v, const void *lambda,
+                               const int32_t *q_len, const int32_t *kv_len, const void *out,
+                               const void *out2, const float *lse, const void *dout, void *dq,
+                               void *dk, void *dv, void *dlambda, void *workspace, size_t ws_bytes,
+                               sla_stream_t stream);
+
+/*
+ * sla_prefix_forward -- attention of B sequences over P shared prefix keys and
+ * then their own: out = softmax(tau q [k_prefix; k]^T) [v_prefix; v], or with
+ * p->differential = 1 (lambda given, else NULL) the difference of two such maps
+ * as in sla_diff_forward.  Where the sequences have few queries, the queries of
+ * all of them take the prefix together, so that it is read once for the batch,
+ * and the parts are joined by their log-sum-exps.  P = 0 (k_prefix, v_prefix
+ * NULL) is ordinary attention, Nk = 0 (k, v NULL) attention to the prefix alone.
+ * lse is written if not NULL.  strides: 16 values, of q (3), k_prefix (2),
+ * v_prefix (2), k (3), v (3), out (3).
+ */
+sla_status_t sla_prefix_forward(const sla_dense_params_t *p, const int64_t *strides, const void *q,
+                                const void *k_prefix, const void *v_prefix, const void *k,
+                                const void *v, const void *lambda, const int32_t *q_len,
+                                const int32_t *kv_len, void *out, float *lse, void *workspace,
+                                size_t ws_bytes, sla_stream_t stream);
+
 /* Static text for a status code. */
 const char *sla_status_string(sla_status_t s);
 
@@ -329,7 +435,9 @@ typedef enum {
                                    kernel (router, pre-pass and their joins)     */
     SLA_KERNEL_COCLUSTER = 10,  /* the co-clustering kernels of one call          */
     SLA_KERNEL_PERMUTE = 11,    /* row permutation (co-clustered order)           */
-    SLA_KERNEL_KINDS = 12
+    SLA_KERNEL_DENSE = 12,      /* dense attention, and the join of its parts     */
+    SLA_KERNEL_DENSE_BWD = 13,  /* gradients of differential attention            */
+    SLA_KERNEL_KINDS = 14
 } sla_kernel_kind_t;
 
 sla_status_t sla_profile_enable(int32_t on);
