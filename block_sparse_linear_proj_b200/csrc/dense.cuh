@@ -1,6 +1,9 @@
 // dense.cuh -- dense attention: differential attention with its gradients, and
 // attention over a shared prefix.
 #pragma once
+#include <type_traits>
+
+#include "attn.cuh"
 #include "common.cuh"
 
 namespace sla {
@@ -52,79 +55,567 @@ __device__ __forceinline__ int dense_len(const int32_t* len, int b, int most) {
     return n;
 }
 
-// ------------------------------------------------------------------ one warp a row
-// Forward: lane = key for the logits, lane = D/32 columns for the products.
+// ------------------------------------------------------------------ forward
+// One CTA owns up to 256 query rows of one key/value head and walks a range of
+// 128-key tiles with two softmax streams, a warpgroup each:
+//   plain, many rows  stream s = rows [128 s, 128 s + 128), every tile
+//   plain, <= 128     both streams the same rows, stream s the tiles of parity s
+//   differential      stream s = map s of the same 128 rows, every tile
+// Stream s: S_s = Q K^T (tcgen05, M = N = 128, fp32 in tensor memory; map s
+// contracts its half of the head), one row a thread: running maximum and sum in
+// fp32, P in 16 bits written over the first columns of S_s, O_s += P V.  While
+// one stream is in its softmax the tensor core works for the other:
+//   P_0 V, S_0', P_1 V, S_1', ...   (in issue order, so S_s' may overwrite P_s)
+// S_s(i) complete implies P_s(i-1) V complete, so a row may rescale O_s then; it
+// does so only when its maximum has grown by 2^8 (P stays below 2^8, exact in
+// the sum; the reference maximum cancels in O / l).
+// Rows are (query i, head g of the group) in the order i * G + g, so a causal
+// tile ends early and the heads of a group share each key tile.  Key tiles come
+// from the prefix first, then the sequence's own keys.  Where sequences have few
+// rows, "gathered" CTAs take the rows of all sequences against the prefix, and
+// the prefix is read once; their parts and those of split ranges are joined by
+// dense_merge_kernel.
+// Value rows past a sequence's length may hold anything (and 0 * NaN is NaN):
+// they are zeroed in shared memory.
+// Warps: w0 TMA producer, w1 MMA issuer, w4-11 the two streams.
+constexpr int kDenseBN = 128;
+constexpr int kDenseThreads = 384;
+
+struct DenseMaps {
+    CUtensorMap k, v, kp, vp;      // [B, Hk, N, D] 16-bit, box 64 x 128 tokens
+};
+
+struct DenseFwdArgs {
+    DenseArgs a;
+    int k_b, k_h, v_b, v_h, kp_h, vp_h;   // 0: that dimension is broadcast in the map
+    int gathered_items, tiles_g, splits_g, two_g;  // gathered CTAs: prefix only
+    int tiles_b, splits_b, two_b;                  // CTAs of one sequence
+    int prefix_b;                                  // these walk the prefix too
+    int direct;                                    // one part: results, else parts
+    float* opart;                                  // [slot][map][row][D] fp32
+    float* lpart;                                  // [slot][map][row] log2 units
+    int slots_g, slots_b;
+    long long rows;                                // B * Hk * G * Nq
+    unsigned long long wait_ns;
+};
+
+template <int D, bool DIFF>
+struct DenseFwdLayout {
+    static constexpr int NQ = DIFF ? 1 : 2;
+    static constexpr int BOX = 128 * 128;                 // 64 columns of 128 rows
+    static constexpr int TILE = 128 * D * 2;
+    static constexpr int SLOTS = D == 128 ? (DIFF ? 6 : 5) : 8;
+    static constexpr int OFF_RING = NQ * TILE;
+    static constexpr int OFF_MISC = OFF_RING + SLOTS * TILE;
+    static constexpr int SMEM = 1024 + OFF_MISC + 256 + (DIFF ? 2 * 128 * 4 : 0);
+    static_assert(SMEM <= 232448, "shared memory of an SM");
+};
+
+__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int n, int h,
+                                            int b) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(n), "r"(h), "r"(b)
+        : "memory");
+}
+template <int N>
+__device__ __forceinline__ void reg_inc() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void reg_dec() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+__device__ __forceinline__ uint64_t fadd2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi);
+template <>
+__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float lo, float hi) { return pack_bf16(lo, hi); }
+template <>
+__device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) { return pack_half2(lo, hi); }
+template <typename T>
+__host__ __device__ constexpr uint32_t idesc_t(int M, int N, int a_mn, int b_mn) {
+    return std::is_same<T, __half>::value ? idesc_f16(M, N, a_mn, b_mn) : idesc_bf16(M, N, a_mn, b_mn);
+}
+
+// Maximum of 128 floats in four register arrays.
+__device__ __forceinline__ float max128(const uint32_t (&v)[4][32]) {
+    float a[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        a[i] = fmax3(__uint_as_float(v[0][i]), __uint_as_float(v[0][8 + i]), __uint_as_float(v[0][16 + i]));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) a[i] = fmax3(a[i], __uint_as_float(v[0][24 + i]), __uint_as_float(v[1][i]));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) a[i] = fmax3(a[i], __uint_as_float(v[1][8 + i]), __uint_as_float(v[1][16 + i]));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) a[i] = fmax3(a[i], __uint_as_float(v[1][24 + i]), __uint_as_float(v[2][i]));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) a[i] = fmax3(a[i], __uint_as_float(v[2][8 + i]), __uint_as_float(v[2][16 + i]));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) a[i] = fmax3(a[i], __uint_as_float(v[2][24 + i]), __uint_as_float(v[3][i]));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) a[i] = fmax3(a[i], __uint_as_float(v[3][8 + i]), __uint_as_float(v[3][16 + i]));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) a[i] = fmaxf(a[i], __uint_as_float(v[3][24 + i]));
+    return fmax3(fmax3(a[0], a[1], a[2]), fmax3(a[3], a[4], a[5]), fmaxf(a[6], a[7]));
+}
+
+// Own keys that query i of a sequence sees: [0, this).
+__device__ __forceinline__ int dense_own(int i, int qn, int kn, int causal) {
+    return causal ? min(kn, max(0, i + kn - qn + 1)) : kn;
+}
+
 template <int D, typename T, bool DIFF>
-__global__ void __launch_bounds__(128) dense_fwd_rows_kernel(const DenseArgs a) {
-    constexpr int C = D / 32, M = DIFF ? 2 : 1, E = D / M;
-    __shared__ float qs[4][D];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const long long row = static_cast<long long>(blockIdx.x) * 4 + warp;
-    if (row >= static_cast<long long>(a.B) * a.H * a.Nq) return;
-    const int i = row % a.Nq, h = row / a.Nq % a.H, b = row / a.Nq / a.H, hk = h / a.G;
-    const int qn = dense_len(a.q_len, b, a.Nq), kn = dense_len(a.kv_len, b, a.Nk);
-    float m[M], l[M], acc[M][C];
-    for (int x = 0; x < M; ++x) {
-        m[x] = -INFINITY;
-        l[x] = 0.f;
-        for (int c = 0; c < C; ++c) acc[x][c] = 0.f;
+__global__ void __launch_bounds__(kDenseThreads, 1)
+    dense_fwd_kernel(const __grid_constant__ DenseMaps tm, const __grid_constant__ DenseFwdArgs f) {
+    using L = DenseFwdLayout<D, DIFF>;
+    constexpr int NBOX = D / 64, SLOTS = L::SLOTS;
+    constexpr uint32_t COL_O = 256;
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    unsigned char* smem = reinterpret_cast<unsigned char*>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    const uint32_t sbase = smem_u32(smem);
+    const DenseArgs& a = f.a;
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::OFF_MISC);   // [SLOTS]
+    uint64_t* empty = full + SLOTS;                                     // [SLOTS]
+    uint64_t* q_full = empty + SLOTS;
+    uint64_t* s_full = q_full + 1;                                      // [2]
+    uint64_t* p_full = s_full + 2;                                      // [2]
+    uint64_t* o_full = p_full + 2;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(o_full + 1);
+    volatile int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
+    float* xl = reinterpret_cast<float*>(smem + L::OFF_MISC + 256);     // [2][128] differential: 1 / row sums
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    // ------------------------------------------------------------ which rows, which keys
+    const bool gathered = static_cast<int>(blockIdx.x) < f.gathered_items;
+    int it = gathered ? blockIdx.x : blockIdx.x - f.gathered_items;
+    const int splits = gathered ? f.splits_g : f.splits_b, tiles = gathered ? f.tiles_g : f.tiles_b;
+    const bool two = DIFF ? false : (gathered ? f.two_g : f.two_b) != 0;       // two row tiles
+    const int sp = it % splits;
+    it /= splits;
+    int tile, hk, b0;
+    if (gathered) {
+        tile = it % tiles, hk = it / tiles, b0 = 0;
+    } else {           // a head's key tiles stay in L2 while its row tiles run; the longest causal rows first
+        tile = tiles - 1 - it % tiles;
+        it /= tiles;
+        hk = it % a.Hk, b0 = it / a.Hk;
     }
-    if (i < qn) {
-        for (int c = lane; c < D; c += 32)
-            qs[warp][c] = to_f<T>(static_cast<const T*>(a.q)[a.qs.at(b, h, i) + c]);
-        __syncwarp();
-        const int own = a.causal ? min(kn, max(0, i + kn - qn + 1)) : kn;
-        for (int part = 0; part < 2; ++part) {
-            const int n = part ? own : a.P;
-            const T* kb = static_cast<const T*>(part ? a.k : a.kp) + (part ? a.ks.at(b, hk, 0) : a.kps.at(0, hk, 0));
-            const T* vb = static_cast<const T*>(part ? a.v : a.vp) + (part ? a.vs.at(b, hk, 0) : a.vps.at(0, hk, 0));
-            const long long kst = part ? a.ks.n : a.kps.n, vst = part ? a.vs.n : a.vps.n;
-            for (int j0 = 0; j0 < n; j0 += 32) {
-                const int j = j0 + lane;
-                float s[M], p[M];
-                for (int x = 0; x < M; ++x) {
-                    s[x] = -INFINITY;
-                    if (j < n) {
-                        s[x] = 0.f;
-                        for (int c = 0; c < E; ++c)
-                            s[x] = fmaf(qs[warp][x * E + c], to_f<T>(kb[j * kst + x * E + c]), s[x]);
-                        s[x] *= a.scale_log2;
-                    }
-                    float mx = s[x];
-                    for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, o));
-                    mx = fmaxf(mx, m[x]);
-                    const float r = exp2f(m[x] - mx);
-                    p[x] = exp2f(s[x] - mx);
-                    m[x] = mx;
-                    float sum = p[x];
-                    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
-                    l[x] = l[x] * r + sum;
-                    for (int c = 0; c < C; ++c) acc[x][c] *= r;
+    const int per_seq = a.G * a.Nq;
+    const int rows = gathered ? a.B * per_seq : per_seq;
+    const int row0 = tile * (two ? 256 : 128);
+    const int qn0 = gathered ? 0 : dense_len(a.q_len, b0, a.Nq), kn0 = gathered ? 0 : dense_len(a.kv_len, b0, a.Nk);
+    const int nP = (gathered || f.prefix_b) ? (a.P + kDenseBN - 1) / kDenseBN : 0;
+    int own = 0;                                   // own keys that the last query of these rows sees
+    if (!gathered) {
+        const int i_last = min(min(rows, row0 + (two ? 256 : 128)) - 1, rows - 1) / a.G;
+        own = dense_own(min(i_last, qn0 - 1), qn0, kn0, a.causal);
+    }
+    const bool any_row = gathered || row0 / a.G < qn0;
+    const int total = any_row ? nP + (own + kDenseBN - 1) / kDenseBN : 0;
+    const int t_begin = static_cast<int>(static_cast<long long>(total) * sp / splits),
+              n = static_cast<int>(static_cast<long long>(total) * (sp + 1) / splits) - t_begin;
+    // the one tile that holds value rows past the sequence's length
+    const int dirty = (!gathered && kn0 < a.Nk && kn0 % kDenseBN != 0) ? nP + kn0 / kDenseBN - t_begin : -1;
+
+    if (tid == 0) {
+        for (int s = 0; s < SLOTS; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        mbar_init(q_full, 8);
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&s_full[s], 1);
+            mbar_init(&p_full[s], 4);
+        }
+        mbar_init(o_full, 1);
+        *abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(tmem_slot, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const unsigned long long lim = f.wait_ns, drain_lim = 4000000000ull;
+    auto fail = [&]() {
+        *abort_flag = 1;
+        report(kStatusTimeout);
+    };
+    auto ring = [&](int x) { return sbase + L::OFF_RING + (x % SLOTS) * L::TILE; };
+
+    if (warp < 4) {
+        reg_dec<56>();
+        if (warp == 0 && lane == 0) {
+            // ================================================ producer: K(0), V(0), K(1), V(1), ...
+            int x = 0;
+            bool ok = true;
+            for (; ok && x < 2 * n; ++x) {
+                const int s = x % SLOTS;
+                if (x >= SLOTS && !mbar_wait(&empty[s], (x / SLOTS - 1) & 1, abort_flag, lim)) {
+                    ok = false;
+                    break;
                 }
-                for (int t = 0; t < min(32, n - j0); ++t)
-                    for (int c = 0; c < C; ++c) {
-                        const float vv = to_f<T>(vb[(j0 + t) * vst + lane + 32 * c]);
-                        for (int x = 0; x < M; ++x)
-                            acc[x][c] = fmaf(__shfl_sync(~0u, p[x], t), vv, acc[x][c]);
+                const int t = t_begin + (x >> 1);
+                const bool pre = t < nP, val = x & 1;
+                const CUtensorMap* m = pre ? (val ? &tm.vp : &tm.kp) : (val ? &tm.v : &tm.k);
+                const int tok = (pre ? t : t - nP) * kDenseBN;
+                const int h = hk * (pre ? (val ? f.vp_h : f.kp_h) : (val ? f.v_h : f.k_h));
+                const int b = pre ? 0 : b0 * (val ? f.v_b : f.k_b);
+                mbar_arrive_expect_tx(&full[s], L::TILE);
+                for (int c = 0; c < NBOX; ++c)
+                    tma_load_4d(smem + L::OFF_RING + s * L::TILE + c * L::BOX, m, &full[s], c * 64, tok, h, b);
+            }
+            if (!ok) fail();
+            for (int y = max(0, x - SLOTS); y < x; ++y)     // every load has landed before the CTA exits
+                mbar_wait(&full[y % SLOTS], (y / SLOTS) & 1, abort_flag, drain_lim);
+        } else if (warp == 1 && lane == 0) {
+            // ================================================ MMA issuer
+            constexpr uint32_t ID_S = idesc_t<T>(128, 128, 0, 0), ID_O = idesc_t<T>(128, D, 0, 1);
+            bool ok = n == 0 || mbar_wait(q_full, 0, abort_flag, lim);
+            tc_fence_after();
+            auto qk = [&](int s, int i) {
+                const uint32_t qb = sbase + (two ? s * L::TILE : 0), kb = ring(2 * i);
+                constexpr int STEPS = DIFF ? D / 32 : D / 16;
+#pragma unroll
+                for (int k = 0; k < STEPS; ++k) {
+                    const int kk = k + (DIFF ? s * STEPS : 0);
+                    const uint32_t off = (kk >> 2) * L::BOX + (kk & 3) * 32;
+                    umma_f16_ss(tmem + s * 128, sdesc(qb + off, 16, 1024, kSwizzle128B),
+                                sdesc(kb + off, 16, 1024, kSwizzle128B), ID_S, k > 0 ? 1u : 0u);
+                }
+                umma_commit(&s_full[s]);
+            };
+            auto pv = [&](int s, int i, bool first) {
+                const uint32_t vb = ring(2 * i + 1);
+#pragma unroll
+                for (int k = 0; k < kDenseBN / 16; ++k)
+                    umma_f16_ts(tmem + COL_O + s * D, tmem + s * 128 + k * 8,
+                                sdesc(vb + k * 2048, L::BOX, 1024, kSwizzle128B), ID_O, (!first || k > 0) ? 1u : 0u);
+            };
+            auto have = [&](int x) { return mbar_wait(&full[x % SLOTS], (x / SLOTS) & 1, abort_flag, lim); };
+            auto done = [&](int x) { umma_commit(&empty[x % SLOTS]); };
+            if (DIFF || two) {
+                for (int i = 0; ok && i <= n; ++i) {
+                    for (int s = 0; ok && s < 2; ++s) {
+                        if (i > 0) {
+                            if ((s == 0 && !have(2 * i - 1)) || !mbar_wait(&p_full[s], (i - 1) & 1, abort_flag, lim)) {
+                                ok = false;
+                                break;
+                            }
+                            tc_fence_after();
+                            pv(s, i - 1, i == 1);
+                            if (s == 1) done(2 * i - 1);
+                        }
+                        if (i < n) {
+                            if (s == 0 && !have(2 * i)) {
+                                ok = false;
+                                break;
+                            }
+                            tc_fence_after();
+                            qk(s, i);
+                            if (s == 1) done(2 * i);
+                        }
                     }
+                }
+            } else {
+                for (int i = 0; ok && i < n + 2; ++i) {
+                    const int s = i & 1, j = i - 2;
+                    if (j >= 0 && j < n) {
+                        if (!have(2 * j + 1) || !mbar_wait(&p_full[s], (j >> 1) & 1, abort_flag, lim)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        pv(s, j, j < 2);
+                        done(2 * j + 1);
+                    }
+                    if (i < n) {
+                        if (!have(2 * i)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        qk(s, i);
+                        done(2 * i);
+                    }
+                }
+            }
+            if (!ok) fail();
+            umma_commit(o_full);           // also: every MMA has completed before tensor memory is released
+            mbar_wait(o_full, 0, abort_flag, drain_lim);
+        }
+    } else {
+        reg_inc<224>();
+        // ==================================================== streams
+        const int q4 = warp & 3, s = (warp - 4) >> 2, r = q4 * 32 + lane;
+        const uint32_t tl = tmem + (static_cast<uint32_t>(q4 * 32) << 16);
+        auto wwait = [&](uint64_t* bar, uint32_t par) {
+            return __all_sync(~0u, mbar_wait(bar, par, abort_flag, lim) ? 1 : 0) != 0;
+        };
+        // the query rows, 16 bytes a thread: zeros where there is no query
+        if (n > 0) {
+            constexpr int CH = D / 8;                           // 16-byte chunks a row
+            const int nrow = two ? 256 : 128;
+            for (int x = tid - 128; x < nrow * CH; x += 256) {
+                const int rr = x / CH, c = x % CH, gr = row0 + rr;
+                uint4 val = make_uint4(0, 0, 0, 0);
+                if (gr < rows) {
+                    const int b = gathered ? gr / per_seq : b0, lr = gathered ? gr % per_seq : gr;
+                    const int i = lr / a.G, g = lr % a.G;
+                    if (i < (gathered ? dense_len(a.q_len, b, a.Nq) : qn0))
+                        val = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) +
+                                                                   a.qs.at(b, hk * a.G + g, i) + c * 8));
+                }
+                *reinterpret_cast<uint4*>(smem + (rr >> 7) * L::TILE + (c >> 3) * L::BOX + sw128(rr & 127, c & 7)) = val;
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(q_full);
+        }
+        // this thread's row
+        const int gr = row0 + (two ? s * 128 : 0) + r;
+        const bool in = gr < rows;
+        const int b = gathered ? (in ? gr / per_seq : 0) : b0, lr = gathered ? gr % per_seq : gr;
+        const int qi = lr / a.G, h = hk * a.G + lr % a.G;
+        const bool real = in && qi < (gathered ? dense_len(a.q_len, b, a.Nq) : qn0);
+        const int own_r = gathered ? 0 : dense_own(qi, qn0, kn0, a.causal);
+        const float c = a.scale_log2, grow = 8.f / c;
+        float m = -INFINITY, l = 0.f;                           // reference maximum (raw logits), sum
+        bool ok = true;
+        const int step = (DIFF || two) ? 1 : 2;
+        int u = 0;
+        for (int i = step == 2 ? s : 0; i < n; i += step, ++u) {
+            if (!wwait(&s_full[s], u & 1)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            uint32_t sv[4][32];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) tmem_ld32(tl + s * 128 + x * 32, sv[x]);
+            tmem_ld_wait();
+            const int t = t_begin + i;
+            const int see = t < nP ? a.P - t * kDenseBN : own_r - (t - nP) * kDenseBN;   // columns this row sees
+            if (__any_sync(~0u, see < kDenseBN)) {
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+#pragma unroll
+                    for (int y = 0; y < 32; ++y)
+                        if (x * 32 + y >= see) sv[x][y] = 0xFF800000u;       // -inf
+            }
+            const float mx = max128(sv);
+            const bool up = mx > m + grow || (m == -INFINITY && mx > m);
+            if (__any_sync(~0u, up)) {
+                const float to = up ? mx : m;
+                const float k = up ? fast_exp2((m - to) * c) : 1.f;            // 0 from -inf
+                l *= k;
+                m = to;
+                if (u > 0) {
+#pragma unroll 1
+                    for (int x = 0; x < D; x += 32) {
+                        uint32_t o[32];
+                        tmem_ld32(tl + COL_O + s * D + x, o);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * k);
+                        tmem_st32(tl + COL_O + s * D + x, o);
+                    }
+                }
+            }
+            const float nm = m == -INFINITY ? 0.f : -m * c;
+            const uint64_t c2 = f2pack(c, c), nm2 = f2pack(nm, nm);
+            uint64_t sum0 = 0, sum1 = 0;
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                uint32_t pw[16];
+#pragma unroll
+                for (int y = 0; y < 16; ++y) {
+                    float lo, hi;
+                    f2unpack(ffma2(f2pack(__uint_as_float(sv[x][2 * y]), __uint_as_float(sv[x][2 * y + 1])), c2, nm2), lo,
+                             hi);
+                    lo = fast_exp2(lo);
+                    hi = fast_exp2(hi);
+                    if (y & 1) sum1 = fadd2(sum1, f2pack(lo, hi));
+                    else sum0 = fadd2(sum0, f2pack(lo, hi));
+                    pw[y] = pack2<T>(lo, hi);
+                }
+                tmem_st16(tl + s * 128 + x * 16, pw);
+            }
+            float s0, s1;
+            f2unpack(fadd2(sum0, sum1), s0, s1);
+            l += s0 + s1;
+            if (i == dirty && (s == 0 || step == 2)) {
+                // value rows past the sequence's length to zero, before this stream's P is announced.  (The slot's
+                // barrier is in this use's phase: the use before it was consumed before S of this tile.)
+                const int x = 2 * i + 1, r0 = kn0 % kDenseBN;
+                if (!wwait(&full[x % SLOTS], (x / SLOTS) & 1)) {
+                    ok = false;
+                    break;
+                }
+                unsigned char* vt = smem + L::OFF_RING + (x % SLOTS) * L::TILE + r0 * 128;
+                for (int y = r; y < (128 - r0) * 8; y += 128)
+#pragma unroll
+                    for (int bx = 0; bx < NBOX; ++bx)
+                        *reinterpret_cast<uint4*>(vt + bx * L::BOX + y * 16) = make_uint4(0, 0, 0, 0);
+                fence_proxy_async_smem();
+            }
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&p_full[s]);
+        }
+        if (!ok) fail();
+        // ---------------------------------------------------- results
+        ok = wwait(o_full, 0) && ok;
+        tc_fence_after();
+        if (!real) l = 0.f;
+        const float lse2 = l > 0.f ? m * c + log2f(l) : -INFINITY;
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+        const long long prow = (static_cast<long long>(b) * a.Hk + hk) * per_seq + lr;
+        constexpr int M = DIFF ? 2 : 1;
+        // parts: [slot][map][row]; a plain stream of its own tiles is a slot of its own
+        const int slot = (gathered ? 0 : f.slots_g) + (step == 2 ? 2 * sp + s : sp);
+        if (f.direct) {
+            if (in && a.lse) a.lse[((static_cast<long long>(b) * a.H + h) * M + (DIFF ? s : 0)) * a.Nq + qi] =
+                lse2 * 0.6931471805599453f;
+        } else if (in) {
+            f.lpart[(static_cast<long long>(slot) * M + (DIFF ? s : 0)) * f.rows + prow] = lse2;
+        }
+        if (DIFF && f.direct) {
+            // both maps' factors of this row, then half of its columns a warpgroup
+            xl[s * 128 + r] = inv;
+            named_bar(1, 256);
+            const float i1 = xl[r], lam = to_f<T>(static_cast<const T*>(a.lam)[h]), i2 = xl[128 + r];
+            T* op = static_cast<T*>(a.out) + a.os.at(b, h, qi);
+            T* o2p = a.out2 ? static_cast<T*>(a.out2) + ((static_cast<long long>(b) * a.H + h) * a.Nq + qi) * D : nullptr;
+#pragma unroll 1
+            for (int x = s * (D / 2); x < (s + 1) * (D / 2); x += 32) {
+                uint32_t o1[32], o2[32];
+                tmem_ld32(tl + COL_O + x, o1);
+                tmem_ld32(tl + COL_O + D + x, o2);
+                tmem_ld_wait();
+                uint32_t w1[16], w2[16];
+#pragma unroll
+                for (int y = 0; y < 16; ++y) {
+                    const float a0 = i2 > 0.f ? __uint_as_float(o2[2 * y]) * i2 : 0.f,
+                                a1 = i2 > 0.f ? __uint_as_float(o2[2 * y + 1]) * i2 : 0.f;
+                    const float b0_ = i1 > 0.f ? __uint_as_float(o1[2 * y]) * i1 : 0.f,
+                                b1_ = i1 > 0.f ? __uint_as_float(o1[2 * y + 1]) * i1 : 0.f;
+                    w1[y] = pack2<T>(fmaf(-lam, a0, b0_), fmaf(-lam, a1, b1_));
+                    w2[y] = pack2<T>(a0, a1);
+                }
+                if (in && ok) {
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        reinterpret_cast<uint4*>(op + x)[y] = make_uint4(w1[4 * y], w1[4 * y + 1], w1[4 * y + 2], w1[4 * y + 3]);
+                        if (o2p)
+                            reinterpret_cast<uint4*>(o2p + x)[y] =
+                                make_uint4(w2[4 * y], w2[4 * y + 1], w2[4 * y + 2], w2[4 * y + 3]);
+                    }
+                }
+            }
+        } else {
+            T* op = static_cast<T*>(a.out) + (in ? a.os.at(b, h, qi) : 0);
+            float* pp = f.direct ? nullptr : f.opart + ((static_cast<long long>(slot) * M + (DIFF ? s : 0)) * f.rows + prow) * D;
+            const bool write = in && ok && (f.direct || l > 0.f);
+#pragma unroll 1
+            for (int x = 0; x < D; x += 32) {
+                uint32_t o[32];
+                tmem_ld32(tl + COL_O + s * D + x, o);
+                tmem_ld_wait();
+#pragma unroll
+                for (int y = 0; y < 32; ++y) o[y] = l > 0.f ? __float_as_uint(__uint_as_float(o[y]) * inv) : 0u;
+                if (!write) continue;
+                if (f.direct) {
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int z = 0; z < 4; ++z)
+                            w[z] = pack2<T>(__uint_as_float(o[8 * y + 2 * z]), __uint_as_float(o[8 * y + 2 * z + 1]));
+                        reinterpret_cast<uint4*>(op + x)[y] = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                } else {
+#pragma unroll
+                    for (int y = 0; y < 8; ++y)
+                        reinterpret_cast<uint4*>(pp + x)[y] = make_uint4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
+                }
             }
         }
     }
-    const float lam = DIFF ? to_f<T>(static_cast<const T*>(a.lam)[h]) : 0.f;
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) tmem_dealloc(tmem, 512);
+}
+
+// Joins the parts of each row, a warp a row: weights 2^(lse_p - max), their sum,
+// the weighed mean of the parts' outputs.  Reads each part once.
+template <int D, typename T, bool DIFF>
+__global__ void __launch_bounds__(256) dense_merge_kernel(const __grid_constant__ DenseFwdArgs f) {
+    constexpr int C = D / 32, M = DIFF ? 2 : 1;
+    const DenseArgs& a = f.a;
+    const int lane = threadIdx.x & 31;
+    const long long row = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    if (row >= f.rows) return;
+    const int per_seq = a.G * a.Nq, lr = static_cast<int>(row % per_seq);
+    const int hk = static_cast<int>(row / per_seq % a.Hk), b = static_cast<int>(row / per_seq / a.Hk);
+    const int qi = lr / a.G, h = hk * a.G + lr % a.G;
+    const int slots = f.slots_g + f.slots_b;
+    float o[M][C];
+#pragma unroll
     for (int x = 0; x < M; ++x) {
-        const float inv = l[x] > 0.f ? 1.f / l[x] : 0.f;
-        for (int c = 0; c < C; ++c) acc[x][c] *= inv;
+        float mx = -INFINITY, sum = 0.f;
+        for (int p = lane; p < slots; p += 32) mx = fmaxf(mx, f.lpart[(static_cast<long long>(p) * M + x) * f.rows + row]);
+#pragma unroll
+        for (int y = 16; y; y >>= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, y));
+#pragma unroll
+        for (int c = 0; c < C; ++c) o[x][c] = 0.f;
+        if (mx > -INFINITY) {
+            for (int p = 0; p < slots; ++p) {
+                const long long at = (static_cast<long long>(p) * M + x) * f.rows + row;
+                const float w = fast_exp2(f.lpart[at] - mx);
+                if (!(w > 0.f)) continue;                      // nothing seen there: its output was not written
+                sum += w;
+                const float* src = f.opart + at * D + lane * C;
+#pragma unroll
+                for (int c = 0; c < C; ++c) o[x][c] = fmaf(w, src[c], o[x][c]);
+            }
+            const float inv = 1.f / sum;
+#pragma unroll
+            for (int c = 0; c < C; ++c) o[x][c] *= inv;
+        }
         if (a.lse && lane == 0)
-            a.lse[((static_cast<long long>(b) * a.H + h) * M + x) * a.Nq + i] =
-                l[x] > 0.f ? (m[x] + log2f(l[x])) * 0.6931471805599453f : -INFINITY;
+            a.lse[((static_cast<long long>(b) * a.H + h) * M + x) * a.Nq + qi] =
+                mx > -INFINITY ? (mx + log2f(sum)) * 0.6931471805599453f : -INFINITY;
     }
-    for (int c = 0; c < C; ++c) {
-        static_cast<T*>(a.out)[a.os.at(b, h, i) + lane + 32 * c] =
-            from_f<T>(DIFF ? acc[0][c] - lam * acc[M - 1][c] : acc[0][c]);
-        if (DIFF && a.out2) static_cast<T*>(a.out2)[row * D + lane + 32 * c] = from_f<T>(acc[M - 1][c]);
+    const float lam = DIFF ? to_f<T>(static_cast<const T*>(a.lam)[h]) : 0.f;
+    T* op = static_cast<T*>(a.out) + a.os.at(b, h, qi) + lane * C;
+    T* o2p = DIFF && a.out2 ? static_cast<T*>(a.out2) + ((static_cast<long long>(b) * a.H + h) * a.Nq + qi) * D + lane * C : nullptr;
+#pragma unroll
+    for (int c = 0; c < C; c += 2) {
+        float v0 = o[0][c], v1 = o[0][c + 1];
+        if (DIFF) {
+            v0 = fmaf(-lam, o[M - 1][c], v0);
+            v1 = fmaf(-lam, o[M - 1][c + 1], v1);
+            if (o2p) *reinterpret_cast<uint32_t*>(o2p + c) = pack2<T>(o[M - 1][c], o[M - 1][c + 1]);
+        }
+        *reinterpret_cast<uint32_t*>(op + c) = pack2<T>(v0, v1);
     }
 }
 
+// ------------------------------------------------------------------ gradients
 // delta_1 = dout . (out + lambda out2), delta_2 = dout . out2, one warp a row.
 template <int D, typename T>
 __global__ void __launch_bounds__(128) dense_delta_kernel(const DenseArgs a) {

@@ -4,8 +4,6 @@
 
 namespace {
 
-int dense_es(const sla_dense_params_t*) { return 2; }   // both I/O types have 16 bits
-
 sla_status_t dense_check(const sla_dense_params_t* p) {
     if (!p) return SLA_ERR_INVALID_ARG;
     if (p->B <= 0 || p->H <= 0 || p->Hk <= 0 || p->Nq <= 0 || p->Nk < 0 || p->P < 0 || p->d <= 0)
@@ -48,17 +46,90 @@ sla_status_t dense_strides(const int64_t* st, int nd, int B, int H, int N, int d
     return SLA_OK;
 }
 
+// How the forward call splits its work over CTAs (one an SM: 148 at once).
+struct DensePlan {
+    int tiles_g, splits_g, two_g, slots_g;   // gathered: every sequence's rows against the prefix
+    int tiles_b, splits_b, two_b, slots_b;   // the rows of one sequence
+    int gathered_items, items, prefix_b, direct;
+    long long rows;
+};
+
+DensePlan dense_plan(const sla_dense_params_t* p) {
+    DensePlan x{};
+    const long long G = p->H / p->Hk, seq = G * p->Nq, all = seq * p->B;
+    const bool diff = p->differential != 0;
+    constexpr long long SMS = 148;
+    auto cdiv = [](long long u, long long v) { return (u + v - 1) / v; };
+    const long long nP = cdiv(p->P, sla::kDenseBN), nK = cdiv(p->Nk, sla::kDenseBN);
+    x.rows = all * p->Hk;
+    // The prefix is taken for all sequences at once where a sequence alone leaves most of a row tile empty.
+    const bool gather = p->P > 0 && p->B > 1 && seq < 128;
+    auto shape = [&](long long rows, int& tiles, int& two) {
+        two = !diff && rows > 128;
+        tiles = static_cast<int>(cdiv(rows, two ? 256 : 128));
+    };
+    shape(seq, x.tiles_b, x.two_b);
+    x.prefix_b = !gather;
+    const long long tb = nK + (gather ? 0 : nP), cb = static_cast<long long>(p->B) * p->Hk * x.tiles_b;
+    long long work = cb * tb, cg = 0;
+    if (gather) {
+        shape(all, x.tiles_g, x.two_g);
+        cg = static_cast<long long>(p->Hk) * x.tiles_g;
+        work += cg * nP;
+    }
+    // a range of key tiles a CTA so that all of them run at once, four tiles at least (a CTA's start and the
+    // join cost about as much as that many)
+    const long long share = std::max<long long>(4, cdiv(work, SMS));
+    x.splits_b = static_cast<int>(cb >= SMS ? 1 : std::max<long long>(1, std::min(cdiv(tb, share), SMS / cb)));
+    x.splits_g = gather ? static_cast<int>(std::max<long long>(1, cdiv(nP, share))) : 0;
+    // a stream of every second tile is a part of its own
+    x.slots_b = x.splits_b * (!diff && !x.two_b ? 2 : 1);
+    x.slots_g = gather ? x.splits_g * (!diff && !x.two_g ? 2 : 1) : 0;
+    if (gather && p->Nk == 0) x.slots_b = x.splits_b = 0;
+    x.gathered_items = static_cast<int>(cg * x.splits_g);
+    x.items = x.gathered_items + static_cast<int>(cb * x.splits_b);
+    x.direct = x.slots_b + x.slots_g == 1;
+    return x;
+}
+
 struct DenseWs {
-    size_t delta, total;
+    size_t delta, opart, lpart, total;
 };
 
 DenseWs dense_layout(const sla_dense_params_t* p) {
     DenseWs w{};
+    const DensePlan x = dense_plan(p);
+    const size_t maps = p->differential ? 2 : 1;
+    // the forward's parts and the backward's sums are never in use together
     size_t off = 0;
     auto take = [&](size_t bytes) { size_t o = off; off = align_up(off + bytes); return o; };
-    w.delta = take(2ull * p->B * p->H * p->Nq * 4);
+    if (!x.direct) {
+        const size_t n = static_cast<size_t>(x.slots_b + x.slots_g) * maps * static_cast<size_t>(x.rows);
+        w.opart = take(n * p->d * 4);
+        w.lpart = take(n * 4);
+    }
     w.total = off;
+    off = 0;
+    if (p->differential) w.delta = take(2ull * p->B * p->H * p->Nq * 4);
+    w.total = std::max<size_t>(std::max(w.total, off), kAlign);
     return w;
+}
+
+// 4-D map over a [B, Hk, N, d] tensor of 16-bit values, box 64 x 128 tokens (128-byte swizzle).  A dimension of
+// stride 0 has one entry in the map; the kernel's coordinate there is 0.
+bool dense_map(CUtensorMap* m, const void* base, const sla::DenseT& t, int B, int Hk, int N, int d, bool half) {
+    EncodeFn fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(N),
+                                static_cast<cuuint64_t>(t.h ? Hk : 1), static_cast<cuuint64_t>(t.b ? B : 1)};
+    const cuuint64_t row = static_cast<cuuint64_t>(d) * 2;
+    const cuuint64_t strides[3] = {t.n ? static_cast<cuuint64_t>(t.n) * 2 : row,
+                                   t.h ? static_cast<cuuint64_t>(t.h) * 2 : row,
+                                   t.b ? static_cast<cuuint64_t>(t.b) * 2 : row};
+    const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(sla::kDenseBN), 1, 1}, one[4] = {1, 1, 1, 1};
+    return fn(m, half ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base),
+              dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 sla_status_t dense_check_ws(const sla_dense_params_t* p, void* ws, size_t ws_bytes, DenseWs& w) {
@@ -85,16 +156,46 @@ sla_status_t dense_small(const sla_dense_params_t* p, const void* lambda, const 
     return SLA_OK;
 }
 
-template <int D, typename T>
-sla_status_t dense_fwd(const sla_dense_params_t* p, const sla::DenseArgs& a, cudaStream_t st) {
-    const long long rows = static_cast<long long>(p->B) * p->H * p->Nq;
-    const unsigned grid = static_cast<unsigned>((rows + 3) / 4);
-    Span sp(SLA_KERNEL_DENSE, st);
-    if (p->differential)
-        sla::dense_fwd_rows_kernel<D, T, true><<<grid, 128, 0, st>>>(a);
-    else
-        sla::dense_fwd_rows_kernel<D, T, false><<<grid, 128, 0, st>>>(a);
+template <int D, typename T, bool DIFF>
+sla_status_t dense_fwd_t(const sla_dense_params_t* p, const sla::DenseArgs& a, void* ws, const DenseWs& w,
+                         cudaStream_t st) {
+    using L = sla::DenseFwdLayout<D, DIFF>;
+    const DensePlan x = dense_plan(p);
+    sla::DenseFwdArgs f{};
+    f.a = a;
+    f.k_b = a.ks.b != 0, f.k_h = a.ks.h != 0, f.v_b = a.vs.b != 0, f.v_h = a.vs.h != 0;
+    f.kp_h = a.kps.h != 0, f.vp_h = a.vps.h != 0;
+    f.gathered_items = x.gathered_items, f.tiles_g = x.tiles_g, f.splits_g = x.splits_g, f.two_g = x.two_g;
+    f.tiles_b = x.tiles_b, f.splits_b = x.splits_b, f.two_b = x.two_b, f.prefix_b = x.prefix_b, f.direct = x.direct;
+    f.slots_g = x.slots_g, f.slots_b = x.slots_b, f.rows = x.rows;
+    f.opart = at<float>(ws, w.opart), f.lpart = at<float>(ws, w.lpart);
+    f.wait_ns = wait_limit_ns();
+    sla::DenseMaps tm{};
+    constexpr bool half = std::is_same<T, __half>::value;
+    if (p->Nk && (!dense_map(&tm.k, a.k, a.ks, p->B, p->Hk, p->Nk, D, half) ||
+                  !dense_map(&tm.v, a.v, a.vs, p->B, p->Hk, p->Nk, D, half)))
+        return SLA_ERR_CUDA;
+    if (p->P && (!dense_map(&tm.kp, a.kp, a.kps, 1, p->Hk, p->P, D, half) ||
+                 !dense_map(&tm.vp, a.vp, a.vps, 1, p->Hk, p->P, D, half)))
+        return SLA_ERR_CUDA;
+    auto kern = sla::dense_fwd_kernel<D, T, DIFF>;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM) != cudaSuccess)
+        return SLA_ERR_CUDA;
+    {
+        Span sp(SLA_KERNEL_DENSE, st);
+        kern<<<x.items, sla::kDenseThreads, L::SMEM, st>>>(tm, f);
+    }
+    if (!x.direct) {
+        Span sp(SLA_KERNEL_DENSE, st);
+        sla::dense_merge_kernel<D, T, DIFF><<<static_cast<unsigned>((x.rows + 7) / 8), 256, 0, st>>>(f);
+    }
     return launch_status();
+}
+
+template <int D, typename T>
+sla_status_t dense_fwd(const sla_dense_params_t* p, const sla::DenseArgs& a, void* ws, const DenseWs& w,
+                       cudaStream_t st) {
+    return p->differential ? dense_fwd_t<D, T, true>(p, a, ws, w, st) : dense_fwd_t<D, T, false>(p, a, ws, w, st);
 }
 
 template <int D, typename T>
@@ -159,7 +260,7 @@ extern "C" sla_status_t sla_diff_forward(const sla_dense_params_t* p, const int6
     a.q = q, a.k = k, a.v = v, a.lam = lambda, a.q_len = q_len, a.kv_len = kv_len;
     a.out = out, a.out2 = out2, a.lse = lse;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    return finish(dense_dispatch(p, [&](auto d, auto t) { return dense_fwd<d(), decltype(t)>(p, a, st); }), st);
+    return finish(dense_dispatch(p, [&](auto d, auto t) { return dense_fwd<d(), decltype(t)>(p, a, workspace, w, st); }), st);
 }
 
 extern "C" sla_status_t sla_diff_backward(const sla_dense_params_t* p, const int64_t* strides, const void* q,
@@ -221,5 +322,5 @@ extern "C" sla_status_t sla_prefix_forward(const sla_dense_params_t* p, const in
     a.q = q, a.k = k, a.v = v, a.kp = k_prefix, a.vp = v_prefix, a.lam = lambda;
     a.q_len = q_len, a.kv_len = kv_len, a.out = out, a.lse = lse;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    return finish(dense_dispatch(p, [&](auto d, auto t) { return dense_fwd<d(), decltype(t)>(p, a, st); }), st);
+    return finish(dense_dispatch(p, [&](auto d, auto t) { return dense_fwd<d(), decltype(t)>(p, a, workspace, w, st); }), st);
 }
