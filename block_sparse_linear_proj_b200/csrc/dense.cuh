@@ -28,7 +28,6 @@ struct DenseArgs {
     int causal;
     float scale;                  // tau
     float scale_log2;             // tau * log2(e)
-    float* delta;                 // backward: [2][B * H * Nq]
 };
 
 template <typename T>
@@ -616,124 +615,494 @@ __global__ void __launch_bounds__(256) dense_merge_kernel(const __grid_constant_
 }
 
 // ------------------------------------------------------------------ gradients
-// delta_1 = dout . (out + lambda out2), delta_2 = dout . out2, one warp a row.
-template <int D, typename T>
-__global__ void __launch_bounds__(128) dense_delta_kernel(const DenseArgs a) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const long long rows = static_cast<long long>(a.B) * a.H * a.Nq;
-    const long long row = static_cast<long long>(blockIdx.x) * 4 + warp;
-    if (row >= rows) return;
-    const int i = row % a.Nq, h = row / a.Nq % a.H, b = row / a.Nq / a.H;
-    float d1 = 0.f, d2 = 0.f;
-    if (i < dense_len(a.q_len, b, a.Nq)) {
-        const float lam = to_f<T>(static_cast<const T*>(a.lam)[h]);
-        for (int c = lane; c < D; c += 32) {
-            const float g = to_f<T>(static_cast<const T*>(a.dout)[a.dos.at(b, h, i) + c]);
-            const float o = to_f<T>(static_cast<const T*>(a.out)[a.os.at(b, h, i) + c]);
-            const float o2 = to_f<T>(static_cast<const T*>(a.out2)[row * D + c]);
-            d1 = fmaf(g, fmaf(lam, o2, o), d1);
-            d2 = fmaf(g, o2, d2);
-        }
-    }
-    for (int o = 16; o; o >>= 1) {
-        d1 += __shfl_xor_sync(~0u, d1, o);
-        d2 += __shfl_xor_sync(~0u, d2, o);
-    }
-    if (lane == 0) {
-        a.delta[row] = d1;
-        a.delta[rows + row] = d2;
-    }
-}
-
-// dlambda_h = -sum over batch and queries of delta_2, one block a head, a fixed order.
+// Rows the gradient kernel streams past its resident tile, and what it reads of
+// each query: kDenseRowFloats values for 64 queries, in the order
+//   -lse_1 log2 e + shift | -lse_2 log2 e + shift | -delta_1 2^-shift | -delta_2 2^-shift
+// (-inf, 0 for padding and queries that see nothing, whose weights so become 0).
+// shift is 10 for fp16: P 2^10 keeps the weights of rows of thousands of keys
+// out of the subnormal range (2^-14); W = P_1 - lambda P_2 enters its product
+// scaled and dv is scaled back, dS = (P 2^10) ((dP - delta) 2^-10) is not scaled.
+constexpr int kDenseRowTile = 64, kDenseRowFloats = 4 * kDenseRowTile;
 template <typename T>
-__global__ void __launch_bounds__(256) dense_dlambda_kernel(const DenseArgs a) {
-    __shared__ double part[256];
-    const int h = blockIdx.x;
-    const long long rows = static_cast<long long>(a.B) * a.H * a.Nq;
-    double s = 0.0;
-    for (int b = 0; b < a.B; ++b)
-        for (int i = threadIdx.x; i < a.Nq; i += 256)
-            s += a.delta[rows + (static_cast<long long>(b) * a.H + h) * a.Nq + i];
-    part[threadIdx.x] = s;
-    __syncthreads();
-    for (int o = 128; o; o >>= 1) {
-        if (threadIdx.x < o) part[threadIdx.x] += part[threadIdx.x + o];
-        __syncthreads();
-    }
-    if (threadIdx.x == 0) static_cast<T*>(a.dlam)[h] = from_f<T>(static_cast<float>(-part[0]));
+constexpr float kDenseShift = std::is_same<T, __half>::value ? 10.f : 0.f;
+template <typename T>
+constexpr float kDenseUnshift = std::is_same<T, __half>::value ? 9.765625e-4f : 1.f;
+
+struct DenseBwdArgs {
+    DenseArgs a;
+    int q_b, q_h, do_b, do_h, k_b, k_h, v_b, v_h;   // 0: that dimension is broadcast in the map
+    int key_items, key_tiles, query_tiles;          // CTAs of 128 keys, then CTAs of 128 queries
+    int row_tiles;                                  // ceil(Nq / 64)
+    float* rowdata;                                 // [B * H][row_tiles][kDenseRowFloats]
+    float* dlam_part;                               // [B * H][row_tiles] sums of delta_2
+    unsigned long long wait_ns;
+};
+
+struct DenseBwdMaps {
+    CUtensorMap q, dout, k, v;                      // box 64 x 64 tokens
+};
+
+__device__ __forceinline__ void unpack8(const uint4& w, float (&x)[8], __nv_bfloat16) {
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[2 * i] = bf16lo(u[i]), x[2 * i + 1] = bf16hi(u[i]);
+}
+__device__ __forceinline__ void unpack8(const uint4& w, float (&x)[8], __half) {
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[2 * i] = half_lo(u[i]), x[2 * i + 1] = half_hi(u[i]);
 }
 
-// dq (KEYS = false, a warp a query) or dk and dv (KEYS = true, a warp a key).
-template <int D, typename T, bool KEYS>
-__global__ void __launch_bounds__(128) dense_bwd_rows_kernel(const DenseArgs a) {
-    constexpr int C = D / 32, E = D / 2;
-    __shared__ float xs[4][2 * D];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int heads = KEYS ? a.Hk : a.H, len = KEYS ? a.Nk : a.Nq;
-    const long long rows = static_cast<long long>(a.B) * a.H * a.Nq;
-    const long long row = static_cast<long long>(blockIdx.x) * 4 + warp;
-    if (row >= static_cast<long long>(a.B) * heads * len) return;
-    const int r = row % len, hh = row / len % heads, b = row / len / heads;
-    const int qn = dense_len(a.q_len, b, a.Nq), kn = dense_len(a.kv_len, b, a.Nk);
-    const T *q = static_cast<const T*>(a.q), *k = static_cast<const T*>(a.k), *v = static_cast<const T*>(a.v),
-            *g = static_cast<const T*>(a.dout);
-    float acc[2][C];
-    for (int c = 0; c < C; ++c) acc[0][c] = acc[1][c] = 0.f;
-    if (r < (KEYS ? kn : qn)) {
-        const T* x0 = KEYS ? k + a.ks.at(b, hh, r) : q + a.qs.at(b, hh, r);
-        const T* x1 = KEYS ? v + a.vs.at(b, hh, r) : g + a.dos.at(b, hh, r);
-        for (int c = lane; c < D; c += 32) {
-            xs[warp][c] = to_f<T>(x0[c]);
-            xs[warp][D + c] = to_f<T>(x1[c]);
-        }
-        __syncwarp();
-        for (int gg = 0; gg < (KEYS ? a.G : 1); ++gg) {
-            const int h = KEYS ? hh * a.G + gg : hh, hk = KEYS ? hh : hh / a.G;
-            const float lam = to_f<T>(static_cast<const T*>(a.lam)[h]);
-            const int first = KEYS && a.causal ? max(0, r - kn + qn) : 0;
-            const int last = KEYS ? qn : (a.causal ? min(kn, max(0, r + kn - qn + 1)) : kn);
-            for (int j0 = first; j0 < last; j0 += 32) {
-                const int j = j0 + lane;
-                float w0 = 0.f, ds1 = 0.f, ds2 = 0.f;
-                if (j < last) {
-                    const T* y0 = KEYS ? q + a.qs.at(b, h, j) : k + a.ks.at(b, hk, j);
-                    const T* y1 = KEYS ? g + a.dos.at(b, h, j) : v + a.vs.at(b, hk, j);
-                    float s1 = 0.f, s2 = 0.f, dp = 0.f;
-                    for (int c = 0; c < E; ++c) {
-                        s1 = fmaf(xs[warp][c], to_f<T>(y0[c]), s1);
-                        s2 = fmaf(xs[warp][E + c], to_f<T>(y0[E + c]), s2);
-                    }
-                    for (int c = 0; c < D; ++c) dp = fmaf(xs[warp][D + c], to_f<T>(y1[c]), dp);
-                    const int qi = KEYS ? j : r;
-                    const long long at = (static_cast<long long>(b) * a.H + h) * a.Nq + qi;
-                    const float* ls = a.lse + (static_cast<long long>(b) * a.H + h) * 2 * a.Nq + qi;
-                    const float p1 = expf(s1 * a.scale - ls[0]), p2 = expf(s2 * a.scale - ls[a.Nq]);
-                    w0 = p1 - lam * p2;
-                    ds1 = a.scale * p1 * (dp - a.delta[at]);
-                    ds2 = -lam * a.scale * p2 * (dp - a.delta[rows + at]);
-                }
-                for (int t = 0; t < min(32, last - j0); ++t) {
-                    const float t0 = __shfl_sync(~0u, w0, t), t1 = __shfl_sync(~0u, ds1, t),
-                                t2 = __shfl_sync(~0u, ds2, t);
-                    const T* y0 = KEYS ? q + a.qs.at(b, h, j0 + t) : k + a.ks.at(b, hk, j0 + t);
-                    const T* y1 = g + (KEYS ? a.dos.at(b, h, j0 + t) : 0);
-                    for (int c = 0; c < C; ++c) {
-                        acc[0][c] = fmaf(lane + 32 * c < E ? t1 : t2, to_f<T>(y0[lane + 32 * c]), acc[0][c]);
-                        if (KEYS) acc[1][c] = fmaf(t0, to_f<T>(y1[lane + 32 * c]), acc[1][c]);
-                    }
+// The per-query values above, from one read of dout, out and out2:
+//   delta_2 = dout . out2,  delta_1 = dout . O_1 = dout . out + lambda delta_2.
+// One CTA a tile of 64 queries of a head, 8 lanes a row.
+template <int D, typename T>
+__global__ void __launch_bounds__(256) dense_rows_kernel(const __grid_constant__ DenseBwdArgs f) {
+    const DenseArgs& a = f.a;
+    __shared__ float part[8];
+    const int t = blockIdx.x % f.row_tiles, bh = blockIdx.x / f.row_tiles, h = bh % a.H, b = bh / a.H;
+    const int qn = dense_len(a.q_len, b, a.Nq), lane8 = threadIdx.x & 7;
+    const float lam = to_f<T>(static_cast<const T*>(a.lam)[h]);
+    float sum2 = 0.f;
+#pragma unroll
+    for (int y = 0; y < 2; ++y) {
+        const int c = y * 32 + (threadIdx.x >> 3), i = t * kDenseRowTile + c;
+        float d1 = 0.f, d2 = 0.f;
+        if (i < qn) {
+            const T* g = static_cast<const T*>(a.dout) + a.dos.at(b, h, i);
+            const T* o = static_cast<const T*>(a.out) + a.os.at(b, h, i);
+            const T* o2 = static_cast<const T*>(a.out2) + (static_cast<long long>(bh) * a.Nq + i) * D;
+#pragma unroll
+            for (int x = 0; x < D / 64; ++x) {
+                const int at = (x * 8 + lane8) * 8;
+                float gv[8], ov[8], o2v[8];
+                unpack8(__ldg(reinterpret_cast<const uint4*>(g + at)), gv, T{});
+                unpack8(__ldg(reinterpret_cast<const uint4*>(o + at)), ov, T{});
+                unpack8(__ldg(reinterpret_cast<const uint4*>(o2 + at)), o2v, T{});
+#pragma unroll
+                for (int z = 0; z < 8; ++z) {
+                    d1 = fmaf(gv[z], ov[z], d1);
+                    d2 = fmaf(gv[z], o2v[z], d2);
                 }
             }
         }
-    }
-    for (int c = 0; c < C; ++c) {
-        if (KEYS) {
-            static_cast<T*>(a.dk)[a.dks.at(b, hh, r) + lane + 32 * c] = from_f<T>(acc[0][c]);
-            static_cast<T*>(a.dv)[a.dvs.at(b, hh, r) + lane + 32 * c] = from_f<T>(acc[1][c]);
-        } else {
-            static_cast<T*>(a.dq)[a.dqs.at(b, hh, r) + lane + 32 * c] = from_f<T>(acc[0][c]);
+#pragma unroll
+        for (int x = 4; x; x >>= 1) {
+            d1 += __shfl_xor_sync(~0u, d1, x);
+            d2 += __shfl_xor_sync(~0u, d2, x);
+        }
+        if (lane8 == 0) {
+            float l1 = -INFINITY, l2 = -INFINITY;
+            if (i < qn) {
+                const float* ls = a.lse + static_cast<long long>(bh) * 2 * a.Nq + i;
+                l1 = ls[0], l2 = ls[a.Nq];
+            }
+            const bool some = l1 > -INFINITY;
+            float* row = f.rowdata + (static_cast<long long>(bh) * f.row_tiles + t) * kDenseRowFloats + c;
+            row[0] = some ? kDenseShift<T> - l1 * 1.4426950408889634f : -INFINITY;
+            row[64] = some ? kDenseShift<T> - l2 * 1.4426950408889634f : -INFINITY;
+            row[128] = -fmaf(lam, d2, d1) * kDenseUnshift<T>;
+            row[192] = -d2 * kDenseUnshift<T>;
+            sum2 += d2;
         }
     }
+#pragma unroll
+    for (int x = 16; x; x >>= 1) sum2 += __shfl_xor_sync(~0u, sum2, x);
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = sum2;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        float s = 0.f;
+        for (int x = 0; x < 8; ++x) s += part[x];
+        f.dlam_part[static_cast<long long>(bh) * f.row_tiles + t] = s;
+    }
+}
+
+// One CTA holds 128 rows of one side (X, Y) and streams 64-row tiles of the other
+// (x, y) past them; S_m and dP are recomputed by each side:
+//   keys     X = K, Y = V, x = Q, y = dout:   dv += W^T y,  dk_m += dS_m^T x_m
+//   queries  X = Q, Y = dout, x = K, y = V:   dq_m += dS_m x_m
+// so no sums cross CTAs and the gradients are the same bits every time.  In both
+// the tile is held with the resident row in the tensor-memory lane (for keys
+// that is S^T), so W and dS, written by the thread of their row in 16 bits, are
+// the A operands of the accumulating products: W and dS_1 from tensor memory;
+// dS_2 from shared memory for keys, whose accumulators leave no columns for it.
+//   S_m = X_m x_m^T, dP = Y y^T      tcgen05 M = 128, N = 64, both from shared memory
+// S(i+1) is issued once both warpgroups have read S(i) into registers, and runs
+// while they form the weights of tile i: a warpgroup takes 32 of the 64 columns.
+// At N = 64 the S and dP products read shared memory at 1.5 times their math time.
+// Warps: w0 TMA producer, w1 MMA issuer, w4-11 two warpgroups.
+template <int D>
+struct DenseBwdLayout {
+    static constexpr int RBOX = 128 * 128, SBOX = 64 * 128;   // 64 columns of 128 / 64 rows
+    static constexpr int RES = 128 * D * 2;                    // a resident tile
+    static constexpr int STR = 64 * D * 2;                     // a streamed tile
+    static constexpr int STAGE = 2 * STR + 1024;               // x, y, row values
+    static constexpr int SLOTS = D == 128 ? 4 : 6;
+    static constexpr int OFF_DS2 = 2 * RES;                    // keys: dS_2, 128 rows of 64 values
+    static constexpr int OFF_RING = OFF_DS2 + 16384;
+    static constexpr int OFF_MISC = OFF_RING + SLOTS * STAGE;
+    static constexpr int SMEM = 1024 + OFF_MISC + 256;
+    static_assert(SMEM <= 232448, "shared memory of an SM");
+};
+
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                     smem_u32(dst)),
+                 "l"(src), "r"(bytes), "r"(smem_u32(bar))
+                 : "memory");
+}
+__device__ __forceinline__ uint64_t fmul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+template <int D, typename T, bool KEYS>
+__device__ __forceinline__ void dense_bwd_cta(const DenseBwdMaps& tm, const DenseBwdArgs& f, unsigned char* smem,
+                                              int item) {
+    using L = DenseBwdLayout<D>;
+    constexpr int NBOX = D / 64, SLOTS = L::SLOTS;
+    // tensor memory: S_1 | S_2 | dP | W (keys) or dS_2 | dS_1 | accumulators
+    constexpr uint32_t COL_DP = 128, COL_W = 192, COL_DS1 = 224, COL_ACC = 256;
+    // accumulators: keys dv first; then dk or dq: for d = 128 one of D columns (map m in its half), for d = 64
+    // one for each map over all 64 columns of x, of which its half is the result (N = 64 either way)
+    constexpr uint32_t COL_G = COL_ACC + (KEYS ? D : 0);
+    const uint32_t sbase = smem_u32(smem);
+    const DenseArgs& a = f.a;
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::OFF_MISC);   // [SLOTS]
+    uint64_t* empty = full + SLOTS;                                     // [SLOTS]
+    uint64_t* r_full = empty + SLOTS;     // resident tiles
+    uint64_t* s_full = r_full + 1;        // S, dP of a tile
+    uint64_t* s_free = s_full + 1;        // read by the warpgroups
+    uint64_t* p_full = s_free + 1;        // W, dS written
+    uint64_t* p_free = p_full + 1;        // and consumed
+    uint64_t* end_bar = p_free + 1;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(end_bar + 1);
+    volatile int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tiles = KEYS ? f.key_tiles : f.query_tiles, heads = KEYS ? a.Hk : a.H;
+    // the tiles with the most visible partners first: early keys, late queries
+    const int tile = KEYS ? item % tiles : tiles - 1 - item % tiles;
+    const int hr = item / tiles % heads, b = item / tiles / heads;
+    const int hk = KEYS ? hr : hr / a.G;
+    const int row0 = tile * 128;
+    const int qn = dense_len(a.q_len, b, a.Nq), kn = dense_len(a.kv_len, b, a.Nk), off = kn - qn;
+    int t0 = 0, per = 0;                  // streamed tiles [t0, t0 + per) of each head
+    if (KEYS) {
+        if (row0 < kn) {
+            const int first = a.causal ? max(0, row0 - off) : 0;
+            t0 = first / 64;
+            per = max(0, (qn + 63) / 64 - t0);
+        }
+    } else if (row0 < qn) {
+        per = (dense_own(min(row0 + 127, qn - 1), qn, kn, a.causal) + 63) / 64;
+    }
+    const int n = per * (KEYS ? a.G : 1);
+    // the streamed tile that holds rows past the sequence's length
+    const int slen = KEYS ? qn : kn;
+    const int dirty = slen < (KEYS ? a.Nq : a.Nk) && slen % 64 != 0 ? slen / 64 : -1;
+
+    if (tid == 0) {
+        for (int s = 0; s < SLOTS; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        mbar_init(r_full, 1);
+        mbar_init(s_full, 1);
+        mbar_init(s_free, 8);
+        mbar_init(p_full, 8);
+        mbar_init(p_free, 1);
+        mbar_init(end_bar, 1);
+        *abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(tmem_slot, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const unsigned long long lim = f.wait_ns, drain_lim = 4000000000ull;
+    auto fail = [&]() {
+        *abort_flag = 1;
+        report(kStatusTimeout);
+    };
+    auto stage = [&](int i) { return L::OFF_RING + (i % SLOTS) * L::STAGE; };
+
+    if (warp == 0) {
+        if (lane == 0 && n > 0) {
+            // ================================================ producer
+            const CUtensorMap *mX = KEYS ? &tm.k : &tm.q, *mY = KEYS ? &tm.v : &tm.dout;
+            const CUtensorMap *mx = KEYS ? &tm.q : &tm.k, *my = KEYS ? &tm.dout : &tm.v;
+            const int Xh = hr * (KEYS ? f.k_h : f.q_h), Xb = b * (KEYS ? f.k_b : f.q_b);
+            const int Yh = hr * (KEYS ? f.v_h : f.do_h), Yb = b * (KEYS ? f.v_b : f.do_b);
+            mbar_arrive_expect_tx(r_full, 2 * L::RES);
+            for (int c = 0; c < NBOX; ++c)
+                for (int z = 0; z < 2; ++z) {
+                    tma_load_4d(smem + c * L::RBOX + z * L::SBOX, mX, r_full, c * 64, row0 + z * 64, Xh, Xb);
+                    tma_load_4d(smem + L::RES + c * L::RBOX + z * L::SBOX, mY, r_full, c * 64, row0 + z * 64, Yh, Yb);
+                }
+            bool ok = true;
+            int i = 0;
+            for (; i < n; ++i) {
+                const int s = i % SLOTS, t = t0 + i % per, h = KEYS ? hr * a.G + i / per : hk;
+                if (i >= SLOTS && !mbar_wait(&empty[s], (i / SLOTS - 1) & 1, abort_flag, lim)) {
+                    ok = false;
+                    break;
+                }
+                unsigned char* st = smem + stage(i);
+                mbar_arrive_expect_tx(&full[s], 2 * L::STR + (KEYS ? kDenseRowFloats * 4 : 0));
+                const int xh = h * (KEYS ? f.q_h : f.k_h), xb = b * (KEYS ? f.q_b : f.k_b);
+                const int yh = h * (KEYS ? f.do_h : f.v_h), yb = b * (KEYS ? f.do_b : f.v_b);
+                for (int c = 0; c < NBOX; ++c) {
+                    tma_load_4d(st + c * L::SBOX, mx, &full[s], c * 64, t * 64, xh, xb);
+                    tma_load_4d(st + L::STR + c * L::SBOX, my, &full[s], c * 64, t * 64, yh, yb);
+                }
+                if (KEYS)
+                    bulk_load(st + 2 * L::STR,
+                              f.rowdata + ((static_cast<long long>(b) * a.H + h) * f.row_tiles + t) * kDenseRowFloats,
+                              kDenseRowFloats * 4, &full[s]);
+            }
+            if (!ok) fail();
+            mbar_wait(r_full, 0, abort_flag, drain_lim);    // every load has landed before the CTA exits
+            for (int y = max(0, i - SLOTS); y < i; ++y)
+                mbar_wait(&full[y % SLOTS], (y / SLOTS) & 1, abort_flag, drain_lim);
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            // ================================================ MMA issuer
+            constexpr uint32_t ID_S = idesc_t<T>(128, 64, 0, 0), ID_V = idesc_t<T>(128, D, 0, 1),
+                               ID_G = idesc_t<T>(128, 64, 0, 1);
+            bool ok = n == 0 || mbar_wait(r_full, 0, abort_flag, lim);
+            for (int i = 0; ok && n > 0 && i <= n; ++i) {
+                if (i < n) {
+                    if (!mbar_wait(&full[i % SLOTS], (i / SLOTS) & 1, abort_flag, lim) ||
+                        (i > 0 && !mbar_wait(s_free, (i - 1) & 1, abort_flag, lim))) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t x = sbase + stage(i), y = x + L::STR;
+                    constexpr int STEPS = D / 32;
+#pragma unroll
+                    for (int kk = 0; kk < 2 * STEPS; ++kk)
+                        umma_f16_ss(tmem + (kk / STEPS) * 64,
+                                    sdesc(sbase + (kk >> 2) * L::RBOX + (kk & 3) * 32, 16, 1024, kSwizzle128B),
+                                    sdesc(x + (kk >> 2) * L::SBOX + (kk & 3) * 32, 16, 1024, kSwizzle128B), ID_S,
+                                    kk % STEPS ? 1u : 0u);
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk)
+                        umma_f16_ss(tmem + COL_DP,
+                                    sdesc(sbase + L::RES + (kk >> 2) * L::RBOX + (kk & 3) * 32, 16, 1024, kSwizzle128B),
+                                    sdesc(y + (kk >> 2) * L::SBOX + (kk & 3) * 32, 16, 1024, kSwizzle128B), ID_S,
+                                    kk ? 1u : 0u);
+                    umma_commit(s_full);
+                }
+                if (i > 0) {
+                    const int j = i - 1;
+                    if (!mbar_wait(p_full, j & 1, abort_flag, lim)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t x = sbase + stage(j), y = x + L::STR;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const uint32_t acc = j > 0 || k > 0 ? 1u : 0u;
+                        if (KEYS)
+                            umma_f16_ts(tmem + COL_ACC, tmem + COL_W + k * 8,
+                                        sdesc(y + k * 2048, L::SBOX, 1024, kSwizzle128B), ID_V, acc);
+                        umma_f16_ts(tmem + COL_G, tmem + COL_DS1 + k * 8,
+                                    sdesc(x + k * 2048, L::SBOX, 1024, kSwizzle128B), ID_G, acc);
+                        const uint64_t x2 = sdesc(x + (D == 128 ? L::SBOX : 0) + k * 2048, L::SBOX, 1024, kSwizzle128B);
+                        if (KEYS)
+                            umma_f16_ss(tmem + COL_G + 64, sdesc(sbase + L::OFF_DS2 + k * 32, 16, 1024, kSwizzle128B), x2,
+                                        ID_G, acc);
+                        else
+                            umma_f16_ts(tmem + COL_G + 64, tmem + COL_W + k * 8, x2, ID_G, acc);
+                    }
+                    umma_commit(p_free);
+                    umma_commit(&empty[j % SLOTS]);
+                }
+            }
+            if (!ok) fail();
+            umma_commit(end_bar);          // also: every MMA has completed before tensor memory is released
+            mbar_wait(end_bar, 0, abort_flag, drain_lim);
+        }
+    } else if (warp == 3) {
+        // dlambda_h = -sum over batch and queries of delta_2, in a fixed order: one CTA a head
+        if (!KEYS && b == 0 && tile == 0) {
+            double s = 0.0;
+            for (long long x = lane; x < static_cast<long long>(a.B) * f.row_tiles; x += 32)
+                s += f.dlam_part[(x / f.row_tiles * a.H + hr) * f.row_tiles + x % f.row_tiles];
+#pragma unroll
+            for (int x = 16; x; x >>= 1) s += __shfl_xor_sync(~0u, s, x);
+            if (lane == 0) static_cast<T*>(a.dlam)[hr] = from_f<T>(static_cast<float>(-s));
+        }
+    } else if (warp >= 4) {
+        // ==================================================== warpgroups
+        const int q4 = warp & 3, w = (warp - 4) >> 2, r = q4 * 32 + lane;
+        const uint32_t tl = tmem + (static_cast<uint32_t>(q4 * 32) << 16);
+        auto wwait = [&](uint64_t* bar, uint32_t par) {
+            return __all_sync(~0u, mbar_wait(bar, par, abort_flag, lim) ? 1 : 0) != 0;
+        };
+        const int row = row0 + r;
+        const float c = a.scale_log2;
+        const uint64_t c2 = f2pack(c, c), un2 = f2pack(kDenseUnshift<T>, kDenseUnshift<T>);
+        uint64_t nl1 = 0, nl2 = 0, nd1 = 0, nd2 = 0;          // queries: this row's values
+        if (!KEYS && n > 0) {
+            const int t = row >> 6;
+            const bool have = t < f.row_tiles;
+            const float* rd = f.rowdata + ((static_cast<long long>(b) * a.H + hr) * f.row_tiles + (have ? t : 0)) *
+                                              kDenseRowFloats + (row & 63);
+            const float v0 = have ? rd[0] : -INFINITY, v1 = have ? rd[64] : -INFINITY, v2 = have ? rd[128] : 0.f,
+                        v3 = have ? rd[192] : 0.f;
+            nl1 = f2pack(v0, v0), nl2 = f2pack(v1, v1), nd1 = f2pack(v2, v2), nd2 = f2pack(v3, v3);
+        }
+        const int own = dense_own(row, qn, kn, a.causal);     // queries
+        float lam = KEYS ? 0.f : to_f<T>(static_cast<const T*>(a.lam)[hr]);
+        bool ok = true;
+        for (int i = 0; i < n; ++i) {
+            const int t = t0 + i % per, base = t * 64 + w * 32;
+            if (KEYS && i % per == 0) lam = to_f<T>(static_cast<const T*>(a.lam)[hr * a.G + i / per]);
+            const uint64_t lam2 = f2pack(lam, lam), neg2 = f2pack(-1.f, -1.f);
+            // (keys: this thread reads the tile's row values itself, so it also waits for their load)
+            if (!wwait(s_full, i & 1) || (KEYS && !wwait(&full[i % SLOTS], (i / SLOTS) & 1))) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            uint32_t s1[32], s2[32], dp[32];
+            tmem_ld32(tl + w * 32, s1);
+            tmem_ld32(tl + 64 + w * 32, s2);
+            tmem_ld32(tl + COL_DP + w * 32, dp);
+            tmem_ld_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(s_free);
+            // columns [lo, hi) count; the others may hold anything
+            const int lo = KEYS && a.causal ? row - off - base : 0;
+            const int hi = KEYS ? (t == dirty ? qn - base : 32) : own - base;
+            if (__any_sync(~0u, lo > 0 || hi < 32)) {
+#pragma unroll
+                for (int x = 0; x < 32; ++x)
+                    if (x < lo || x >= hi) {
+                        s1[x] = s2[x] = 0xFF800000u;          // -inf: weight 0
+                        dp[x] = 0u;
+                    }
+            }
+            unsigned char* st = smem + stage(i);
+            const float* rd = reinterpret_cast<const float*>(st + 2 * L::STR) + w * 32;
+            uint32_t ww[16], d1[16], d2[16];
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {
+                uint64_t l1[2], l2[2], e1[2], e2[2];
+                if (KEYS) {
+                    const ulonglong2 u1 = *reinterpret_cast<const ulonglong2*>(rd + 4 * x);
+                    const ulonglong2 u2 = *reinterpret_cast<const ulonglong2*>(rd + 64 + 4 * x);
+                    const ulonglong2 u3 = *reinterpret_cast<const ulonglong2*>(rd + 128 + 4 * x);
+                    const ulonglong2 u4 = *reinterpret_cast<const ulonglong2*>(rd + 192 + 4 * x);
+                    l1[0] = u1.x, l1[1] = u1.y, l2[0] = u2.x, l2[1] = u2.y;
+                    e1[0] = u3.x, e1[1] = u3.y, e2[0] = u4.x, e2[1] = u4.y;
+                } else {
+                    l1[0] = l1[1] = nl1, l2[0] = l2[1] = nl2, e1[0] = e1[1] = nd1, e2[0] = e2[1] = nd2;
+                }
+#pragma unroll
+                for (int z = 0; z < 2; ++z) {
+                    const int y = 2 * x + z, k = 2 * y;
+                    float u, v;
+                    f2unpack(ffma2(f2pack(__uint_as_float(s1[k]), __uint_as_float(s1[k + 1])), c2, l1[z]), u, v);
+                    const uint64_t p1 = f2pack(fast_exp2(u), fast_exp2(v));
+                    f2unpack(ffma2(f2pack(__uint_as_float(s2[k]), __uint_as_float(s2[k + 1])), c2, l2[z]), u, v);
+                    const uint64_t p2 = fmul2(f2pack(fast_exp2(u), fast_exp2(v)), lam2);
+                    const uint64_t g = f2pack(__uint_as_float(dp[k]), __uint_as_float(dp[k + 1]));
+                    f2unpack(fmul2(p1, ffma2(g, un2, e1[z])), u, v);
+                    d1[y] = pack2<T>(u, v);
+                    f2unpack(fmul2(p2, ffma2(g, un2, e2[z])), u, v);
+                    d2[y] = pack2<T>(-u, -v);
+                    if (KEYS) {
+                        f2unpack(ffma2(p2, neg2, p1), u, v);
+                        ww[y] = pack2<T>(u, v);
+                    }
+                }
+            }
+            // the last tile's products have read W and dS
+            if (i > 0) {
+                if (!wwait(p_free, (i - 1) & 1)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+            }
+            tmem_st16(tl + COL_DS1 + w * 16, d1);
+            if (KEYS) {
+                tmem_st16(tl + COL_W + w * 16, ww);
+#pragma unroll
+                for (int y = 0; y < 4; ++y)
+                    *reinterpret_cast<uint4*>(smem + L::OFF_DS2 + sw128(r, w * 4 + y)) =
+                        make_uint4(d2[4 * y], d2[4 * y + 1], d2[4 * y + 2], d2[4 * y + 3]);
+            } else {
+                tmem_st16(tl + COL_W + w * 16, d2);
+            }
+            if (t == dirty) {      // rows past the length to zero: they are B operands of the products below
+                const int rz = slen % 64;
+                for (int y = w * 128 + r; y < (64 - rz) * 8; y += 256)
+#pragma unroll
+                    for (int bx = 0; bx < 2 * NBOX; ++bx)
+                        *reinterpret_cast<uint4*>(st + bx * L::SBOX + rz * 128 + y * 16) = make_uint4(0, 0, 0, 0);
+            }
+            if (KEYS || t == dirty) fence_proxy_async_smem();
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(p_full);
+        }
+        if (!ok) fail();
+        ok = wwait(end_bar, 0) && ok;
+        tc_fence_after();
+        // ---------------------------------------------------- results: keys dv (w = 0) and dk (w = 1), queries halves of dq
+        const bool in = row < (KEYS ? a.Nk : a.Nq), some = n > 0 && row < (KEYS ? kn : qn);
+        const int x0 = KEYS ? 0 : w * (D / 2), x1 = KEYS ? D : x0 + D / 2;
+        const bool is_v = KEYS && w == 0;
+        const float k = is_v ? kDenseUnshift<T> : a.scale;
+        T* dst = static_cast<T*>(KEYS ? (is_v ? a.dv : a.dk) : a.dq) +
+                 (in ? (KEYS ? (is_v ? a.dvs.at(b, hr, row) : a.dks.at(b, hr, row)) : a.dqs.at(b, hr, row)) : 0);
+#pragma unroll 1
+        for (int x = x0; x < x1; x += 32) {
+            uint32_t o[32];
+            // d = 64: the second map's half lies in its own accumulator
+            tmem_ld32(tl + (is_v ? COL_ACC : COL_G + (D == 64 && x >= 32 ? 64 : 0)) + x, o);
+            tmem_ld_wait();
+            if (in && ok)
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                    uint32_t u[4];
+#pragma unroll
+                    for (int z = 0; z < 4; ++z)
+                        u[z] = some ? pack2<T>(__uint_as_float(o[8 * y + 2 * z]) * k, __uint_as_float(o[8 * y + 2 * z + 1]) * k)
+                                    : 0u;
+                    reinterpret_cast<uint4*>(dst + x)[y] = make_uint4(u[0], u[1], u[2], u[3]);
+                }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) tmem_dealloc(tmem, 512);
+}
+
+template <int D, typename T>
+__global__ void __launch_bounds__(kDenseThreads, 1)
+    dense_bwd_kernel(const __grid_constant__ DenseBwdMaps tm, const __grid_constant__ DenseBwdArgs f) {
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    unsigned char* smem = reinterpret_cast<unsigned char*>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    if (static_cast<int>(blockIdx.x) < f.key_items)
+        dense_bwd_cta<D, T, true>(tm, f, smem, blockIdx.x);
+    else
+        dense_bwd_cta<D, T, false>(tm, f, smem, blockIdx.x - f.key_items);
 }
 
 }  // namespace sla

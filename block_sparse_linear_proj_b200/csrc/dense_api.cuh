@@ -93,7 +93,7 @@ DensePlan dense_plan(const sla_dense_params_t* p) {
 }
 
 struct DenseWs {
-    size_t delta, opart, lpart, total;
+    size_t rowdata, dlam_part, opart, lpart, total;
 };
 
 DenseWs dense_layout(const sla_dense_params_t* p) {
@@ -110,14 +110,19 @@ DenseWs dense_layout(const sla_dense_params_t* p) {
     }
     w.total = off;
     off = 0;
-    if (p->differential) w.delta = take(2ull * p->B * p->H * p->Nq * 4);
+    if (p->differential) {
+        const size_t tiles = static_cast<size_t>(p->B) * p->H * ((p->Nq + sla::kDenseRowTile - 1) / sla::kDenseRowTile);
+        w.rowdata = take(tiles * sla::kDenseRowFloats * 4);
+        w.dlam_part = take(tiles * 4);
+    }
     w.total = std::max<size_t>(std::max(w.total, off), kAlign);
     return w;
 }
 
-// 4-D map over a [B, Hk, N, d] tensor of 16-bit values, box 64 x 128 tokens (128-byte swizzle).  A dimension of
+// 4-D map over a [B, Hk, N, d] tensor of 16-bit values, box 64 x tokens (128-byte swizzle).  A dimension of
 // stride 0 has one entry in the map; the kernel's coordinate there is 0.
-bool dense_map(CUtensorMap* m, const void* base, const sla::DenseT& t, int B, int Hk, int N, int d, bool half) {
+bool dense_map(CUtensorMap* m, const void* base, const sla::DenseT& t, int B, int Hk, int N, int d, bool half,
+               int tokens = sla::kDenseBN) {
     EncodeFn fn = encode_fn();
     if (!fn) return false;
     const cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(N),
@@ -126,7 +131,7 @@ bool dense_map(CUtensorMap* m, const void* base, const sla::DenseT& t, int B, in
     const cuuint64_t strides[3] = {t.n ? static_cast<cuuint64_t>(t.n) * 2 : row,
                                    t.h ? static_cast<cuuint64_t>(t.h) * 2 : row,
                                    t.b ? static_cast<cuuint64_t>(t.b) * 2 : row};
-    const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(sla::kDenseBN), 1, 1}, one[4] = {1, 1, 1, 1};
+    const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(tokens), 1, 1}, one[4] = {1, 1, 1, 1};
     return fn(m, half ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base),
               dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -199,24 +204,36 @@ sla_status_t dense_fwd(const sla_dense_params_t* p, const sla::DenseArgs& a, voi
 }
 
 template <int D, typename T>
-sla_status_t dense_bwd(const sla_dense_params_t* p, const sla::DenseArgs& a, cudaStream_t st) {
-    const long long rows = static_cast<long long>(p->B) * p->H * p->Nq,
-                    keys = static_cast<long long>(p->B) * p->Hk * p->Nk;
+sla_status_t dense_bwd(const sla_dense_params_t* p, const sla::DenseArgs& a, void* ws, const DenseWs& w,
+                       cudaStream_t st) {
+    using L = sla::DenseBwdLayout<D>;
+    sla::DenseBwdArgs f{};
+    f.a = a;
+    f.q_b = a.qs.b != 0, f.q_h = a.qs.h != 0, f.do_b = a.dos.b != 0, f.do_h = a.dos.h != 0;
+    f.k_b = a.ks.b != 0, f.k_h = a.ks.h != 0, f.v_b = a.vs.b != 0, f.v_h = a.vs.h != 0;
+    f.key_tiles = (p->Nk + 127) / 128;
+    f.query_tiles = (p->Nq + 127) / 128;
+    f.row_tiles = (p->Nq + sla::kDenseRowTile - 1) / sla::kDenseRowTile;
+    f.key_items = p->B * p->Hk * f.key_tiles;
+    f.rowdata = at<float>(ws, w.rowdata), f.dlam_part = at<float>(ws, w.dlam_part);
+    f.wait_ns = wait_limit_ns();
+    sla::DenseBwdMaps tm{};
+    constexpr bool half = std::is_same<T, __half>::value;
+    if (!dense_map(&tm.q, a.q, a.qs, p->B, p->H, p->Nq, D, half, 64) ||
+        !dense_map(&tm.dout, a.dout, a.dos, p->B, p->H, p->Nq, D, half, 64) ||
+        (p->Nk && (!dense_map(&tm.k, a.k, a.ks, p->B, p->Hk, p->Nk, D, half, 64) ||
+                   !dense_map(&tm.v, a.v, a.vs, p->B, p->Hk, p->Nk, D, half, 64))))
+        return SLA_ERR_CUDA;
+    auto kern = sla::dense_bwd_kernel<D, T>;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM) != cudaSuccess)
+        return SLA_ERR_CUDA;
     {
         Span sp(SLA_KERNEL_DENSE_BWD, st);
-        sla::dense_delta_kernel<D, T><<<static_cast<unsigned>((rows + 3) / 4), 128, 0, st>>>(a);
+        sla::dense_rows_kernel<D, T><<<p->B * p->H * f.row_tiles, 256, 0, st>>>(f);
     }
     {
         Span sp(SLA_KERNEL_DENSE_BWD, st);
-        sla::dense_dlambda_kernel<T><<<p->H, 256, 0, st>>>(a);
-    }
-    {
-        Span sp(SLA_KERNEL_DENSE_BWD, st);
-        sla::dense_bwd_rows_kernel<D, T, false><<<static_cast<unsigned>((rows + 3) / 4), 128, 0, st>>>(a);
-    }
-    if (keys) {
-        Span sp(SLA_KERNEL_DENSE_BWD, st);
-        sla::dense_bwd_rows_kernel<D, T, true><<<static_cast<unsigned>((keys + 3) / 4), 128, 0, st>>>(a);
+        kern<<<f.key_items + p->B * p->H * f.query_tiles, sla::kDenseThreads, L::SMEM, st>>>(tm, f);
     }
     return launch_status();
 }
@@ -293,9 +310,8 @@ extern "C" sla_status_t sla_diff_backward(const sla_dense_params_t* p, const int
     a.q = q, a.k = k, a.v = v, a.lam = lambda, a.q_len = q_len, a.kv_len = kv_len;
     a.out = const_cast<void*>(out), a.out2 = const_cast<void*>(out2), a.lse = const_cast<float*>(lse);
     a.dout = dout, a.dq = dq, a.dk = dk, a.dv = dv, a.dlam = dlambda;
-    a.delta = at<float>(workspace, w.delta);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    return finish(dense_dispatch(p, [&](auto d, auto t) { return dense_bwd<d(), decltype(t)>(p, a, st); }), st);
+    return finish(dense_dispatch(p, [&](auto d, auto t) { return dense_bwd<d(), decltype(t)>(p, a, workspace, w, st); }), st);
 }
 
 extern "C" sla_status_t sla_prefix_forward(const sla_dense_params_t* p, const int64_t* strides, const void* q,
