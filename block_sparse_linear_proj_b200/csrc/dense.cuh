@@ -62,12 +62,19 @@ __device__ __forceinline__ int dense_len(const int32_t* len, int b, int most) {
 //   differential      stream s = map s of the same 128 rows, every tile
 // Stream s: S_s = Q K^T (tcgen05, M = N = 128, fp32 in tensor memory; map s
 // contracts its half of the head), one row a thread: running maximum and sum in
-// fp32, P in 16 bits written over the first columns of S_s, O_s += P V.  While
-// one stream is in its softmax the tensor core works for the other:
-//   P_0 V, S_0', P_1 V, S_1', ...   (in issue order, so S_s' may overwrite P_s)
-// S_s(i) complete implies P_s(i-1) V complete, so a row may rescale O_s then; it
-// does so only when its maximum has grown by 2^8 (P stays below 2^8, exact in
-// the sum; the reference maximum cancels in O / l).
+// fp32, P in 16 bits written over the first columns of S_s, O_s += P V, its first
+// half while the second half's weights are formed.  While one stream is in its
+// softmax the tensor core works for the other:
+//   S_s(0) | P_s(u) V  S_s(u+1) | ...
+// (in issue order, so S_s(u+1) may overwrite P_s(u), and S_s(u+1) complete means
+// that O_s holds tile u).  A row rescales O_s only when its maximum has grown by
+// 2^8 (P stays below 2^8, exact in the sum; the reference maximum cancels in
+// O / l).  The bound is the special function unit (8 cycles a warp and ex2, 2048
+// for a tile of both streams) beside the tensor core (1536, plain 2048).
+// Measured against this form on the 10400-token differential forward, 1.04 ms:
+// one issuing warp for both streams 1.08, 64-key tiles with two buffers of S
+// 1.15, with four warpgroups 1.10, and a share of the exponentials as polynomials
+// on the FMA pipe (a quarter: 1.06; three eighths: 1.13).
 // Rows are (query i, head g of the group) in the order i * G + g, so a causal
 // tile ends early and the heads of a group share each key tile.  Key tiles come
 // from the prefix first, then the sequence's own keys.  Where sequences have few
@@ -76,7 +83,7 @@ __device__ __forceinline__ int dense_len(const int32_t* len, int b, int most) {
 // dense_merge_kernel.
 // Value rows past a sequence's length may hold anything (and 0 * NaN is NaN):
 // they are zeroed in shared memory.
-// Warps: w0 TMA producer, w1 MMA issuer, w4-11 the two streams.
+// Warps: w0 TMA producer, w1 and w2 MMA issuers of the streams, w4-11 the streams.
 constexpr int kDenseBN = 128;
 constexpr int kDenseThreads = 384;
 
@@ -101,15 +108,46 @@ struct DenseFwdArgs {
 template <int D, bool DIFF>
 struct DenseFwdLayout {
     static constexpr int NQ = DIFF ? 1 : 2;
-    static constexpr int BOX = 128 * 128;                 // 64 columns of 128 rows
-    static constexpr int TILE = 128 * D * 2;
+    static constexpr int QBOX = 128 * 128;                // 64 columns of 128 rows
+    static constexpr int QTILE = 128 * D * 2;
+    static constexpr int BOX = kDenseBN * 128;            // 64 columns of a key tile
+    static constexpr int TILE = kDenseBN * D * 2;
     static constexpr int SLOTS = D == 128 ? (DIFF ? 6 : 5) : 8;
-    static constexpr int OFF_RING = NQ * TILE;
+    static constexpr int OFF_RING = NQ * QTILE;
     static constexpr int OFF_MISC = OFF_RING + SLOTS * TILE;
-    static constexpr int SMEM = 1024 + OFF_MISC + 256 + (DIFF ? 2 * 128 * 4 : 0);
+    static constexpr int SMEM = 1024 + OFF_MISC + 512;
     static_assert(SMEM <= 232448, "shared memory of an SM");
 };
 
+// Bounded wait of a converged warp: all of its lanes, without a branch on the lane (a
+// wait inside one took some 250 cycles longer, measured).
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, uint64_t limit_ns) {
+    return __all_sync(~0u, mbar_wait(bar, parity, abort, limit_ns)) != 0;
+}
+// A place in a ring of mbarrier-guarded slots.  (Kept as slot and phase: quotients
+// and remainders of a running index are long chains of dependent instructions in
+// the issuing warps, whose step time bounds the pipeline.)
+template <int SLOTS>
+struct RingPos {
+    int slot;
+    uint32_t phase;
+    __device__ __forceinline__ void step(int d) {
+        slot += d;
+        if (slot >= SLOTS) {
+            slot -= SLOTS;
+            phase ^= 1u;
+        }
+    }
+};
+// Named barriers between the two streams' warps of a scheduler (ids 2..9).
+__device__ __forceinline__ void turn_wait(int id) { asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory"); }
+__device__ __forceinline__ void turn_give(int id) { asm volatile("bar.arrive %0, 64;" ::"r"(id) : "memory"); }
+// One lane of a converged warp (always the same one).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
 __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int n, int h,
                                             int b) {
     asm volatile(
@@ -142,29 +180,12 @@ __host__ __device__ constexpr uint32_t idesc_t(int M, int N, int a_mn, int b_mn)
     return std::is_same<T, __half>::value ? idesc_f16(M, N, a_mn, b_mn) : idesc_bf16(M, N, a_mn, b_mn);
 }
 
-// Maximum of 128 floats in four register arrays.
-__device__ __forceinline__ float max128(const uint32_t (&v)[4][32]) {
-    float a[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        a[i] = fmax3(__uint_as_float(v[0][i]), __uint_as_float(v[0][8 + i]), __uint_as_float(v[0][16 + i]));
-#pragma unroll
-    for (int i = 0; i < 8; ++i) a[i] = fmax3(a[i], __uint_as_float(v[0][24 + i]), __uint_as_float(v[1][i]));
-#pragma unroll
-    for (int i = 0; i < 8; ++i) a[i] = fmax3(a[i], __uint_as_float(v[1][8 + i]), __uint_as_float(v[1][16 + i]));
-#pragma unroll
-    for (int i = 0; i < 8; ++i) a[i] = fmax3(a[i], __uint_as_float(v[1][24 + i]), __uint_as_float(v[2][i]));
-#pragma unroll
-    for (int i = 0; i < 8; ++i) a[i] = fmax3(a[i], __uint_as_float(v[2][8 + i]), __uint_as_float(v[2][16 + i]));
-#pragma unroll
-    for (int i = 0; i < 8; ++i) a[i] = fmax3(a[i], __uint_as_float(v[2][24 + i]), __uint_as_float(v[3][i]));
-#pragma unroll
-    for (int i = 0; i < 8; ++i) a[i] = fmax3(a[i], __uint_as_float(v[3][8 + i]), __uint_as_float(v[3][16 + i]));
-#pragma unroll
-    for (int i = 0; i < 8; ++i) a[i] = fmaxf(a[i], __uint_as_float(v[3][24 + i]));
-    return fmax3(fmax3(a[0], a[1], a[2]), fmax3(a[3], a[4], a[5]), fmaxf(a[6], a[7]));
+// 2^x for two values.
+__device__ __forceinline__ uint64_t exp2_2(uint64_t x) {
+    float a, b;
+    f2unpack(x, a, b);
+    return f2pack(fast_exp2(a), fast_exp2(b));
 }
-
 // Own keys that query i of a sequence sees: [0, this).
 __device__ __forceinline__ int dense_own(int i, int qn, int kn, int causal) {
     return causal ? min(kn, max(0, i + kn - qn + 1)) : kn;
@@ -184,14 +205,15 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::OFF_MISC);   // [SLOTS]
     uint64_t* empty = full + SLOTS;                                     // [SLOTS]
     uint64_t* q_full = empty + SLOTS;
-    uint64_t* s_full = q_full + 1;                                      // [2]
-    uint64_t* p_full = s_full + 2;                                      // [2]
-    uint64_t* o_full = p_full + 2;
+    uint64_t* s_full = q_full + 1;                                      // [stream]
+    uint64_t* p_full = s_full + 2;                                      // [stream][half]
+    uint64_t* v_here = p_full + 4;                                      // [stream] the dirty tile's values have landed
+    uint64_t* o_full = v_here + 2;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(o_full + 1);
     volatile int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
-    float* xl = reinterpret_cast<float*>(smem + L::OFF_MISC + 256);     // [2][128] differential: 1 / row sums
+    float* xl = reinterpret_cast<float*>(smem + L::OFF_RING);           // [2][128] row sums, after the last product
 
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(~0u, tid >> 5, 0), lane = tid & 31;
 
     // ------------------------------------------------------------ which rows, which keys
     const bool gathered = static_cast<int>(blockIdx.x) < f.gathered_items;
@@ -228,14 +250,16 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
     if (tid == 0) {
         for (int s = 0; s < SLOTS; ++s) {
             mbar_init(&full[s], 1);
-            mbar_init(&empty[s], 1);
+            mbar_init(&empty[s], DIFF || two ? 2 : 1);
         }
         mbar_init(q_full, 8);
         for (int s = 0; s < 2; ++s) {
             mbar_init(&s_full[s], 1);
-            mbar_init(&p_full[s], 4);
+            mbar_init(&p_full[2 * s], 4);
+            mbar_init(&p_full[2 * s + 1], 4);
+            mbar_init(&v_here[s], 1);
         }
-        mbar_init(o_full, 1);
+        mbar_init(o_full, 2);
         *abort_flag = 0;
         fence_barrier_init();
     }
@@ -252,117 +276,115 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
         *abort_flag = 1;
         report(kStatusTimeout);
     };
-    auto ring = [&](int x) { return sbase + L::OFF_RING + (x % SLOTS) * L::TILE; };
+    // Tiles are loaded in the order of their use, K(0) .. K(lead - 1), then V(i), K(i + lead), ...; a K(i + lead) past
+    // the last tile leaves its place empty.  So V(i) has place 2 i + lead, K(i) place i < lead ? i : 2 i - lead + 1.
+    const bool every = DIFF || two;                 // each stream takes every tile
+    const int lead = every ? 1 : 2;
 
-    if (warp < 4) {
-        reg_dec<56>();
-        if (warp == 0 && lane == 0) {
-            // ================================================ producer: K(0), V(0), K(1), V(1), ...
-            int x = 0;
-            bool ok = true;
-            for (; ok && x < 2 * n; ++x) {
-                const int s = x % SLOTS;
-                if (x >= SLOTS && !mbar_wait(&empty[s], (x / SLOTS - 1) & 1, abort_flag, lim)) {
-                    ok = false;
-                    break;
-                }
-                const int t = t_begin + (x >> 1);
-                const bool pre = t < nP, val = x & 1;
+    if (warp < 4) reg_dec<56>();
+    if (warp == 0) {
+        // ==================================================== producer (the whole warp waits, one lane issues)
+        const bool leader = elect_one();
+        RingPos<SLOTS> rp{0, 1u};           // (phase of the wait for an empty slot: the first round passes)
+        uint32_t used = 0u, last = 0u;      // slots loaded, and the phases of their last loads
+        bool ok = true;
+        auto load = [&](int i, bool val) {
+            if (!warp_wait(&empty[rp.slot], rp.phase, abort_flag, lim)) return false;
+            const int t = t_begin + i;
+            const bool pre = t < nP;
+            if (leader) {
                 const CUtensorMap* m = pre ? (val ? &tm.vp : &tm.kp) : (val ? &tm.v : &tm.k);
                 const int tok = (pre ? t : t - nP) * kDenseBN;
                 const int h = hk * (pre ? (val ? f.vp_h : f.kp_h) : (val ? f.v_h : f.k_h));
                 const int b = pre ? 0 : b0 * (val ? f.v_b : f.k_b);
-                mbar_arrive_expect_tx(&full[s], L::TILE);
+                mbar_arrive_expect_tx(&full[rp.slot], L::TILE);
                 for (int c = 0; c < NBOX; ++c)
-                    tma_load_4d(smem + L::OFF_RING + s * L::TILE + c * L::BOX, m, &full[s], c * 64, tok, h, b);
+                    tma_load_4d(smem + L::OFF_RING + rp.slot * L::TILE + c * L::BOX, m, &full[rp.slot], c * 64, tok, h, b);
             }
-            if (!ok) fail();
-            for (int y = max(0, x - SLOTS); y < x; ++y)     // every load has landed before the CTA exits
-                mbar_wait(&full[y % SLOTS], (y / SLOTS) & 1, abort_flag, drain_lim);
-        } else if (warp == 1 && lane == 0) {
-            // ================================================ MMA issuer
-            constexpr uint32_t ID_S = idesc_t<T>(128, 128, 0, 0), ID_O = idesc_t<T>(128, D, 0, 1);
-            bool ok = n == 0 || mbar_wait(q_full, 0, abort_flag, lim);
-            tc_fence_after();
-            auto qk = [&](int s, int i) {
-                const uint32_t qb = sbase + (two ? s * L::TILE : 0), kb = ring(2 * i);
+            __syncwarp();
+            used |= 1u << rp.slot;
+            last = (last & ~(1u << rp.slot)) | ((rp.phase ^ 1u) << rp.slot);
+            return true;
+        };
+        for (int i = 0; ok && i < lead; ++i, rp.step(1))
+            if (i < n) ok = load(i, false);
+        for (int i = 0; ok && i < n; ++i) {
+            ok = load(i, true);
+            rp.step(1);
+            if (ok && i + lead < n) ok = load(i + lead, false);
+            rp.step(1);
+        }
+        if (!ok) fail();
+        for (int y = 0; y < SLOTS; ++y)     // every load has landed before the CTA exits
+            if ((used >> y) & 1u) mbar_wait(&full[y], (last >> y) & 1u, abort_flag, drain_lim);
+    } else if (warp == 1 || warp == 2) {
+        // ==================================================== MMA issuers, one a stream (the whole warp waits, one
+        // lane issues).  An issue blocks until the tensor core takes it, and a wait after it starts only then: with
+        // one issuer for both streams its waits left the tensor core idle for half of the time.
+        const int s = warp - 1;
+        constexpr uint32_t ID_S = idesc_t<T>(128, kDenseBN, 0, 0), ID_O = idesc_t<T>(128, D, 0, 1);
+        const bool leader = elect_one();
+        auto wait = [&](uint64_t* bar, uint32_t par) { return warp_wait(bar, par, abort_flag, lim); };
+        const uint64_t q0 = sdesc(sbase + (two ? s * L::QTILE : 0), 16, 1024, kSwizzle128B),
+                       k0 = sdesc(sbase + L::OFF_RING, 16, 1024, kSwizzle128B),
+                       v0 = sdesc(sbase + L::OFF_RING, L::BOX, 1024, kSwizzle128B);
+        const uint32_t S = tmem + s * 128, O = tmem + COL_O + s * D;
+        const int step = every ? 1 : 2, k_to_v = every ? 1 : 3;
+        RingPos<SLOTS> rp{every ? 0 : s, 0u};
+        // S of the stream's next tile
+        auto qk = [&]() {
+            if (!wait(&full[rp.slot], rp.phase)) return false;
+            if (leader) {
+                const uint64_t kd = k0 + rp.slot * (L::TILE >> 4);
                 constexpr int STEPS = DIFF ? D / 32 : D / 16;
 #pragma unroll
                 for (int k = 0; k < STEPS; ++k) {
                     const int kk = k + (DIFF ? s * STEPS : 0);
-                    const uint32_t off = (kk >> 2) * L::BOX + (kk & 3) * 32;
-                    umma_f16_ss(tmem + s * 128, sdesc(qb + off, 16, 1024, kSwizzle128B),
-                                sdesc(kb + off, 16, 1024, kSwizzle128B), ID_S, k > 0 ? 1u : 0u);
+                    umma_f16_ss(S, q0 + (((kk >> 2) * L::QBOX + (kk & 3) * 32) >> 4),
+                                kd + (((kk >> 2) * L::BOX + (kk & 3) * 32) >> 4), ID_S, k > 0 ? 1u : 0u);
                 }
                 umma_commit(&s_full[s]);
-            };
-            auto pv = [&](int s, int i, bool first) {
-                const uint32_t vb = ring(2 * i + 1);
-#pragma unroll
-                for (int k = 0; k < kDenseBN / 16; ++k)
-                    umma_f16_ts(tmem + COL_O + s * D, tmem + s * 128 + k * 8,
-                                sdesc(vb + k * 2048, L::BOX, 1024, kSwizzle128B), ID_O, (!first || k > 0) ? 1u : 0u);
-            };
-            auto have = [&](int x) { return mbar_wait(&full[x % SLOTS], (x / SLOTS) & 1, abort_flag, lim); };
-            auto done = [&](int x) { umma_commit(&empty[x % SLOTS]); };
-            if (DIFF || two) {
-                for (int i = 0; ok && i <= n; ++i) {
-                    for (int s = 0; ok && s < 2; ++s) {
-                        if (i > 0) {
-                            if ((s == 0 && !have(2 * i - 1)) || !mbar_wait(&p_full[s], (i - 1) & 1, abort_flag, lim)) {
-                                ok = false;
-                                break;
-                            }
-                            tc_fence_after();
-                            pv(s, i - 1, i == 1);
-                            if (s == 1) done(2 * i - 1);
-                        }
-                        if (i < n) {
-                            if (s == 0 && !have(2 * i)) {
-                                ok = false;
-                                break;
-                            }
-                            tc_fence_after();
-                            qk(s, i);
-                            if (s == 1) done(2 * i);
-                        }
-                    }
-                }
-            } else {
-                for (int i = 0; ok && i < n + 2; ++i) {
-                    const int s = i & 1, j = i - 2;
-                    if (j >= 0 && j < n) {
-                        if (!have(2 * j + 1) || !mbar_wait(&p_full[s], (j >> 1) & 1, abort_flag, lim)) {
-                            ok = false;
-                            break;
-                        }
-                        tc_fence_after();
-                        pv(s, j, j < 2);
-                        done(2 * j + 1);
-                    }
-                    if (i < n) {
-                        if (!have(2 * i)) {
-                            ok = false;
-                            break;
-                        }
-                        tc_fence_after();
-                        qk(s, i);
-                        done(2 * i);
-                    }
-                }
+                umma_commit(&empty[rp.slot]);
             }
-            if (!ok) fail();
-            umma_commit(o_full);           // also: every MMA has completed before tensor memory is released
-            mbar_wait(o_full, 0, abort_flag, drain_lim);
+            __syncwarp();
+            return true;
+        };
+        bool ok = n == 0 || wait(q_full, 0);
+        tc_fence_after();
+        int i = every ? 0 : s;
+        if (ok && i < n) ok = qk();
+        rp.step(every ? 1 : 2 + s);
+        for (uint32_t u = 0; ok && i < n; ++u) {
+            // P V of tile i, each half once its weights are there, then S of the stream's next tile
+            if (!(ok = wait(&full[rp.slot], rp.phase))) break;
+            if (i == dirty && leader) mbar_arrive(&v_here[s]);
+            const uint64_t vd = v0 + rp.slot * (L::TILE >> 4);
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                if (!(ok = wait(&p_full[2 * s + half], u & 1))) break;
+                tc_fence_after();
+                if (leader)
+#pragma unroll
+                    for (int k = half * 4; k < half * 4 + 4; ++k)
+                        umma_f16_ts(O, S + k * 8, vd + ((k * 2048) >> 4), ID_O, (u > 0 || k > 0) ? 1u : 0u);
+            }
+            if (!ok) break;
+            if (leader) umma_commit(&empty[rp.slot]);
+            __syncwarp();
+            rp.step(1);
+            if (i + step < n) ok = qk();
+            rp.step(k_to_v);
+            i += step;
         }
-    } else {
+        if (!ok) fail();
+        if (leader) umma_commit(o_full);   // also: every MMA has completed before tensor memory is released
+        mbar_wait(o_full, 0, abort_flag, drain_lim);
+    } else if (warp >= 4) {
         reg_inc<224>();
         // ==================================================== streams
         const int q4 = warp & 3, s = (warp - 4) >> 2, r = q4 * 32 + lane;
         const uint32_t tl = tmem + (static_cast<uint32_t>(q4 * 32) << 16);
-        auto wwait = [&](uint64_t* bar, uint32_t par) {
-            return __all_sync(~0u, mbar_wait(bar, par, abort_flag, lim) ? 1 : 0) != 0;
-        };
+        auto wwait = [&](uint64_t* bar, uint32_t par) { return warp_wait(bar, par, abort_flag, lim); };
         // the query rows, 16 bytes a thread: zeros where there is no query
         if (n > 0) {
             constexpr int CH = D / 8;                           // 16-byte chunks a row
@@ -377,147 +399,170 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
                         val = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) +
                                                                    a.qs.at(b, hk * a.G + g, i) + c * 8));
                 }
-                *reinterpret_cast<uint4*>(smem + (rr >> 7) * L::TILE + (c >> 3) * L::BOX + sw128(rr & 127, c & 7)) = val;
+                *reinterpret_cast<uint4*>(smem + (rr >> 7) * L::QTILE + (c >> 3) * L::QBOX + sw128(rr & 127, c & 7)) = val;
             }
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(q_full);
         }
-        // this thread's row
-        const int gr = row0 + (two ? s * 128 : 0) + r;
-        const bool in = gr < rows;
-        const int b = gathered ? (in ? gr / per_seq : 0) : b0, lr = gathered ? gr % per_seq : gr;
-        const int qi = lr / a.G, h = hk * a.G + lr % a.G;
-        const bool real = in && qi < (gathered ? dense_len(a.q_len, b, a.Nq) : qn0);
-        const int own_r = gathered ? 0 : dense_own(qi, qn0, kn0, a.causal);
+        // this thread's row (asked for again after the loop, which has few registers left)
+        struct Row {
+            int b, lr, qi, h;
+            bool in, real;
+        };
+        auto row_of = [&](int rr) {
+            const int gr = row0 + (two ? s * 128 : 0) + rr;
+            Row x;
+            x.in = gr < rows;
+            x.b = gathered ? (x.in ? gr / per_seq : 0) : b0;
+            x.lr = gathered ? gr % per_seq : gr;
+            x.qi = x.lr / a.G;
+            x.h = hk * a.G + x.lr % a.G;
+            x.real = x.in && x.qi < (gathered ? dense_len(a.q_len, x.b, a.Nq) : qn0);
+            return x;
+        };
+        const int own_r = gathered ? 0 : dense_own(row_of(r).qi, qn0, kn0, a.causal);
         const float c = a.scale_log2, grow = 8.f / c;
         float m = -INFINITY, l = 0.f;                           // reference maximum (raw logits), sum
         bool ok = true;
-        const int step = (DIFF || two) ? 1 : 2;
+        const int step = every ? 1 : 2;
+        // The streams' warps of a scheduler take turns at the exponentials: in lockstep they would share the special
+        // function unit there, and the tensor core elsewhere, and leave each idle half of the time.  A stream that
+        // gave up keeps taking its turns.
+        const int my_turn = 2 + s * 4 + q4, other_turn = 2 + (1 - s) * 4 + q4;
+        if (every && s == 1 && n > 0) turn_give(other_turn);
         int u = 0;
         for (int i = step == 2 ? s : 0; i < n; i += step, ++u) {
-            if (!wwait(&s_full[s], u & 1)) {
-                ok = false;
-                break;
-            }
-            tc_fence_after();
-            uint32_t sv[4][32];
-#pragma unroll
-            for (int x = 0; x < 4; ++x) tmem_ld32(tl + s * 128 + x * 32, sv[x]);
-            tmem_ld_wait();
-            const int t = t_begin + i;
-            const int see = t < nP ? a.P - t * kDenseBN : own_r - (t - nP) * kDenseBN;   // columns this row sees
-            if (__any_sync(~0u, see < kDenseBN)) {
+            const uint32_t sc = tl + s * 128;              // this thread's S, and its P over it
+            uint32_t sv[2][64];
+            ok = ok && wwait(&s_full[s], u & 1);
+            if (ok) {
+                tc_fence_after();
 #pragma unroll
                 for (int x = 0; x < 4; ++x)
+                    tmem_ld32(sc + x * 32, *reinterpret_cast<uint32_t(*)[32]>(&sv[x >> 1][(x & 1) * 32]));
+                tmem_ld_wait();
+                // columns that this row sees
+                const int t = t_begin + i, see = t < nP ? a.P - t * kDenseBN : own_r - (t - nP) * kDenseBN;
+                if (__any_sync(~0u, see < kDenseBN)) {
 #pragma unroll
-                    for (int y = 0; y < 32; ++y)
-                        if (x * 32 + y >= see) sv[x][y] = 0xFF800000u;       // -inf
-            }
-            const float mx = max128(sv);
-            const bool up = mx > m + grow || (m == -INFINITY && mx > m);
-            if (__any_sync(~0u, up)) {
-                const float to = up ? mx : m;
-                const float k = up ? fast_exp2((m - to) * c) : 1.f;            // 0 from -inf
-                l *= k;
-                m = to;
-                if (u > 0) {
+                    for (int y = 0; y < kDenseBN; ++y)
+                        if (y >= see) sv[y >> 6][y & 63] = 0xFF800000u;       // -inf
+                }
+                const float mx = fmaxf(max64_bits(sv[0]), max64_bits(sv[1]));
+                const bool up = mx > m + grow || (m == -INFINITY && mx > m);
+                if (__any_sync(~0u, up)) {
+                    const float to = up ? mx : m, k = up ? fast_exp2((m - to) * c) : 1.f;      // 0 from -inf
+                    l *= k;
+                    m = to;
+                    if (u > 0) {
 #pragma unroll 1
-                    for (int x = 0; x < D; x += 32) {
-                        uint32_t o[32];
-                        tmem_ld32(tl + COL_O + s * D + x, o);
-                        tmem_ld_wait();
+                        for (int x = 0; x < D; x += 32) {
+                            uint32_t o[32];
+                            tmem_ld32(tl + COL_O + s * D + x, o);
+                            tmem_ld_wait();
 #pragma unroll
-                        for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * k);
-                        tmem_st32(tl + COL_O + s * D + x, o);
+                            for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * k);
+                            tmem_st32(tl + COL_O + s * D + x, o);
+                        }
                     }
                 }
-            }
-            const float nm = m == -INFINITY ? 0.f : -m * c;
-            const uint64_t c2 = f2pack(c, c), nm2 = f2pack(nm, nm);
-            uint64_t sum0 = 0, sum1 = 0;
+                if (i == dirty && (ok = wwait(&v_here[s], 0))) {
+                    // value rows past the sequence's length to zero, before this stream's P is announced (each
+                    // stream does it for its own products)
+                    const int x = (2 * i + lead) % SLOTS, r0 = kn0 % kDenseBN;
+                    unsigned char* vt = smem + L::OFF_RING + x * L::TILE + r0 * 128;
+                    for (int y = r; y < (kDenseBN - r0) * 8; y += 128)
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                uint32_t pw[16];
-#pragma unroll
-                for (int y = 0; y < 16; ++y) {
-                    float lo, hi;
-                    f2unpack(ffma2(f2pack(__uint_as_float(sv[x][2 * y]), __uint_as_float(sv[x][2 * y + 1])), c2, nm2), lo,
-                             hi);
-                    lo = fast_exp2(lo);
-                    hi = fast_exp2(hi);
-                    if (y & 1) sum1 = fadd2(sum1, f2pack(lo, hi));
-                    else sum0 = fadd2(sum0, f2pack(lo, hi));
-                    pw[y] = pack2<T>(lo, hi);
+                        for (int bx = 0; bx < NBOX; ++bx)
+                            *reinterpret_cast<uint4*>(vt + bx * L::BOX + y * 16) = make_uint4(0, 0, 0, 0);
+                    fence_proxy_async_smem();
                 }
-                tmem_st16(tl + s * 128 + x * 16, pw);
             }
-            float s0, s1;
-            f2unpack(fadd2(sum0, sum1), s0, s1);
-            l += s0 + s1;
-            if (i == dirty && (s == 0 || step == 2)) {
-                // value rows past the sequence's length to zero, before this stream's P is announced.  (The slot's
-                // barrier is in this use's phase: the use before it was consumed before S of this tile.)
-                const int x = 2 * i + 1, r0 = kn0 % kDenseBN;
-                if (!wwait(&full[x % SLOTS], (x / SLOTS) & 1)) {
-                    ok = false;
-                    break;
-                }
-                unsigned char* vt = smem + L::OFF_RING + (x % SLOTS) * L::TILE + r0 * 128;
-                for (int y = r; y < (128 - r0) * 8; y += 128)
+            if (every) turn_wait(my_turn);
+            if (ok) {
+                const float nm = m == -INFINITY ? 0.f : -m * c;
+                const uint64_t c2 = f2pack(c, c), nm2 = f2pack(nm, nm);
+                uint64_t sum0 = 0, sum1 = 0;
 #pragma unroll
-                    for (int bx = 0; bx < NBOX; ++bx)
-                        *reinterpret_cast<uint4*>(vt + bx * L::BOX + y * 16) = make_uint4(0, 0, 0, 0);
-                fence_proxy_async_smem();
+                for (int x = 0; x < 2; ++x) {
+                    uint32_t pw[32];
+#pragma unroll
+                    for (int y = 0; y < 32; ++y) {
+                        const uint64_t e =
+                            ffma2(f2pack(__uint_as_float(sv[x][2 * y]), __uint_as_float(sv[x][2 * y + 1])), c2, nm2);
+                        const uint64_t w = exp2_2(e);
+                        if (y & 1) sum1 = fadd2(sum1, w);
+                        else sum0 = fadd2(sum0, w);
+                        float lo, hi;
+                        f2unpack(w, lo, hi);
+                        pw[y] = pack2<T>(lo, hi);
+                    }
+                    if (x == 1 && every && (s == 0 || i + 1 < n)) turn_give(other_turn);
+                    tmem_st32(sc + x * 32, pw);
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&p_full[2 * s + x]);
+                }
+                float s0, s1;
+                f2unpack(fadd2(sum0, sum1), s0, s1);
+                l += s0 + s1;
+            } else if (every && (s == 0 || i + 1 < n)) {
+                turn_give(other_turn);
             }
-            tmem_st_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&p_full[s]);
         }
         if (!ok) fail();
         // ---------------------------------------------------- results
         ok = wwait(o_full, 0) && ok;
         tc_fence_after();
-        if (!real) l = 0.f;
+        int again = r;
+        asm volatile("" : "+r"(again));
+        const Row me = row_of(again);
+        const int b = me.b, lr = me.lr, qi = me.qi, h = me.h;
+        const bool in = me.in, real = me.real;
+        if (!real || m == -INFINITY) l = 0.f;
         const float lse2 = l > 0.f ? m * c + log2f(l) : -INFINITY;
-        const float inv = l > 0.f ? 1.f / l : 0.f;
         const long long prow = (static_cast<long long>(b) * a.Hk + hk) * per_seq + lr;
         constexpr int M = DIFF ? 2 : 1;
         // parts: [slot][map][row]; a plain stream of its own tiles is a slot of its own
         const int slot = (gathered ? 0 : f.slots_g) + (step == 2 ? 2 * sp + s : sp);
-        if (f.direct) {
-            if (in && a.lse) a.lse[((static_cast<long long>(b) * a.H + h) * M + (DIFF ? s : 0)) * a.Nq + qi] =
-                lse2 * 0.6931471805599453f;
-        } else if (in) {
-            f.lpart[(static_cast<long long>(slot) * M + (DIFF ? s : 0)) * f.rows + prow] = lse2;
+        const long long part = (static_cast<long long>(slot) * M + (DIFF ? s : 0)) * f.rows + prow;
+        if (in) {
+            if (!f.direct)
+                f.lpart[part] = lse2;
+            else if (a.lse)
+                a.lse[((static_cast<long long>(b) * a.H + h) * M + (DIFF ? s : 0)) * a.Nq + qi] =
+                    lse2 * 0.6931471805599453f;
         }
         if (DIFF && f.direct) {
-            // both maps' factors of this row, then half of its columns a warpgroup
-            xl[s * 128 + r] = inv;
+            // both maps' sums of this row (every product and load is complete: the ring is free), then half of its
+            // columns a warpgroup
+            xl[s * 128 + r] = l;
             named_bar(1, 256);
-            const float i1 = xl[r], lam = to_f<T>(static_cast<const T*>(a.lam)[h]), i2 = xl[128 + r];
-            T* op = static_cast<T*>(a.out) + a.os.at(b, h, qi);
+            const float l1 = xl[r], l2 = xl[128 + r];
+            const float i1 = l1 > 0.f ? 1.f / l1 : 0.f, i2 = l2 > 0.f ? 1.f / l2 : 0.f;
+            const float lam = to_f<T>(static_cast<const T*>(a.lam)[h]);
+            T* op = static_cast<T*>(a.out) + (in ? a.os.at(b, h, qi) : 0);
             T* o2p = a.out2 ? static_cast<T*>(a.out2) + ((static_cast<long long>(b) * a.H + h) * a.Nq + qi) * D : nullptr;
 #pragma unroll 1
-            for (int x = s * (D / 2); x < (s + 1) * (D / 2); x += 32) {
-                uint32_t o1[32], o2[32];
-                tmem_ld32(tl + COL_O + x, o1);
-                tmem_ld32(tl + COL_O + D + x, o2);
+            for (int x = s * (D / 2); x < (s + 1) * (D / 2); x += 16) {
+                uint32_t o1[16], o2[16], w1[8], w2[8];
+                tmem_ld16(tl + COL_O + x, o1);
+                tmem_ld16(tl + COL_O + D + x, o2);
                 tmem_ld_wait();
-                uint32_t w1[16], w2[16];
 #pragma unroll
-                for (int y = 0; y < 16; ++y) {
-                    const float a0 = i2 > 0.f ? __uint_as_float(o2[2 * y]) * i2 : 0.f,
-                                a1 = i2 > 0.f ? __uint_as_float(o2[2 * y + 1]) * i2 : 0.f;
-                    const float b0_ = i1 > 0.f ? __uint_as_float(o1[2 * y]) * i1 : 0.f,
-                                b1_ = i1 > 0.f ? __uint_as_float(o1[2 * y + 1]) * i1 : 0.f;
+                for (int y = 0; y < 8; ++y) {
+                    const float a0 = l2 > 0.f ? __uint_as_float(o2[2 * y]) * i2 : 0.f,
+                                a1 = l2 > 0.f ? __uint_as_float(o2[2 * y + 1]) * i2 : 0.f,
+                                b0_ = l1 > 0.f ? __uint_as_float(o1[2 * y]) * i1 : 0.f,
+                                b1_ = l1 > 0.f ? __uint_as_float(o1[2 * y + 1]) * i1 : 0.f;
                     w1[y] = pack2<T>(fmaf(-lam, a0, b0_), fmaf(-lam, a1, b1_));
                     w2[y] = pack2<T>(a0, a1);
                 }
                 if (in && ok) {
 #pragma unroll
-                    for (int y = 0; y < 4; ++y) {
+                    for (int y = 0; y < 2; ++y) {
                         reinterpret_cast<uint4*>(op + x)[y] = make_uint4(w1[4 * y], w1[4 * y + 1], w1[4 * y + 2], w1[4 * y + 3]);
                         if (o2p)
                             reinterpret_cast<uint4*>(o2p + x)[y] =
@@ -526,20 +571,21 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
                 }
             }
         } else {
+            const float inv = l > 0.f ? 1.f / l : 0.f;
             T* op = static_cast<T*>(a.out) + (in ? a.os.at(b, h, qi) : 0);
-            float* pp = f.direct ? nullptr : f.opart + ((static_cast<long long>(slot) * M + (DIFF ? s : 0)) * f.rows + prow) * D;
+            float* pp = f.direct ? nullptr : f.opart + (in ? part : 0) * D;
             const bool write = in && ok && (f.direct || l > 0.f);
 #pragma unroll 1
-            for (int x = 0; x < D; x += 32) {
-                uint32_t o[32];
-                tmem_ld32(tl + COL_O + s * D + x, o);
+            for (int x = 0; x < D; x += 16) {
+                uint32_t o[16];
+                tmem_ld16(tl + COL_O + s * D + x, o);
                 tmem_ld_wait();
 #pragma unroll
-                for (int y = 0; y < 32; ++y) o[y] = l > 0.f ? __float_as_uint(__uint_as_float(o[y]) * inv) : 0u;
+                for (int y = 0; y < 16; ++y) o[y] = l > 0.f ? __float_as_uint(__uint_as_float(o[y]) * inv) : 0u;
                 if (!write) continue;
                 if (f.direct) {
 #pragma unroll
-                    for (int y = 0; y < 4; ++y) {
+                    for (int y = 0; y < 2; ++y) {
                         uint32_t w[4];
 #pragma unroll
                         for (int z = 0; z < 4; ++z)
@@ -548,7 +594,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
                     }
                 } else {
 #pragma unroll
-                    for (int y = 0; y < 8; ++y)
+                    for (int y = 0; y < 4; ++y)
                         reinterpret_cast<uint4*>(pp + x)[y] = make_uint4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
                 }
             }
@@ -947,7 +993,7 @@ __device__ __forceinline__ void dense_bwd_cta(const DenseBwdMaps& tm, const Dens
         const int q4 = warp & 3, w = (warp - 4) >> 2, r = q4 * 32 + lane;
         const uint32_t tl = tmem + (static_cast<uint32_t>(q4 * 32) << 16);
         auto wwait = [&](uint64_t* bar, uint32_t par) {
-            return __all_sync(~0u, mbar_wait(bar, par, abort_flag, lim) ? 1 : 0) != 0;
+            return warp_wait(bar, par, abort_flag, lim);
         };
         const int row = row0 + r;
         const float c = a.scale_log2;
@@ -1014,10 +1060,10 @@ __device__ __forceinline__ void dense_bwd_cta(const DenseBwdMaps& tm, const Dens
                 for (int z = 0; z < 2; ++z) {
                     const int y = 2 * x + z, k = 2 * y;
                     float u, v;
-                    f2unpack(ffma2(f2pack(__uint_as_float(s1[k]), __uint_as_float(s1[k + 1])), c2, l1[z]), u, v);
-                    const uint64_t p1 = f2pack(fast_exp2(u), fast_exp2(v));
-                    f2unpack(ffma2(f2pack(__uint_as_float(s2[k]), __uint_as_float(s2[k + 1])), c2, l2[z]), u, v);
-                    const uint64_t p2 = fmul2(f2pack(fast_exp2(u), fast_exp2(v)), lam2);
+                    const uint64_t x1 = ffma2(f2pack(__uint_as_float(s1[k]), __uint_as_float(s1[k + 1])), c2, l1[z]);
+                    const uint64_t p1 = exp2_2(x1);
+                    const uint64_t x2 = ffma2(f2pack(__uint_as_float(s2[k]), __uint_as_float(s2[k + 1])), c2, l2[z]);
+                    const uint64_t p2 = fmul2(exp2_2(x2), lam2);
                     const uint64_t g = f2pack(__uint_as_float(dp[k]), __uint_as_float(dp[k + 1]));
                     f2unpack(fmul2(p1, ffma2(g, un2, e1[z])), u, v);
                     d1[y] = pack2<T>(u, v);

@@ -77,8 +77,8 @@ DensePlan dense_plan(const sla_dense_params_t* p) {
         cg = static_cast<long long>(p->Hk) * x.tiles_g;
         work += cg * nP;
     }
-    // a range of key tiles a CTA so that all of them run at once, four tiles at least (a CTA's start and the
-    // join cost about as much as that many)
+    // a range of key tiles a CTA so that all of them run at once, four tiles at least (a CTA's start and
+    // the join cost about as much as that many)
     const long long share = std::max<long long>(4, cdiv(work, SMS));
     x.splits_b = static_cast<int>(cb >= SMS ? 1 : std::max<long long>(1, std::min(cdiv(tb, share), SMS / cb)));
     x.splits_g = gather ? static_cast<int>(std::max<long long>(1, cdiv(nP, share))) : 0;
