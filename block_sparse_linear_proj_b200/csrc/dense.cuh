@@ -680,7 +680,8 @@ struct DenseBwdArgs {
     int key_items, key_tiles, query_tiles;          // CTAs of 128 keys, then CTAs of 128 queries
     int row_tiles;                                  // ceil(Nq / 64)
     float* rowdata;                                 // [B * H][row_tiles][kDenseRowFloats]
-    float* dlam_part;                               // [B * H][row_tiles] sums of delta_2
+    float* dlam_part;                               // [H][B][query_tiles] sums of delta_2
+    unsigned* dlam_done;                            // [H] how many of a head's are there
     unsigned long long wait_ns;
 };
 
@@ -705,11 +706,10 @@ __device__ __forceinline__ void unpack8(const uint4& w, float (&x)[8], __half) {
 template <int D, typename T>
 __global__ void __launch_bounds__(256) dense_rows_kernel(const __grid_constant__ DenseBwdArgs f) {
     const DenseArgs& a = f.a;
-    __shared__ float part[8];
     const int t = blockIdx.x % f.row_tiles, bh = blockIdx.x / f.row_tiles, h = bh % a.H, b = bh / a.H;
     const int qn = dense_len(a.q_len, b, a.Nq), lane8 = threadIdx.x & 7;
     const float lam = to_f<T>(static_cast<const T*>(a.lam)[h]);
-    float sum2 = 0.f;
+    if (b == 0 && t == 0 && threadIdx.x == 0) f.dlam_done[h] = 0u;
 #pragma unroll
     for (int y = 0; y < 2; ++y) {
         const int c = y * 32 + (threadIdx.x >> 3), i = t * kDenseRowTile + c;
@@ -749,17 +749,7 @@ __global__ void __launch_bounds__(256) dense_rows_kernel(const __grid_constant__
             row[64] = some ? kDenseShift<T> - l2 * 1.4426950408889634f : -INFINITY;
             row[128] = -fmaf(lam, d2, d1) * kDenseUnshift<T>;
             row[192] = -d2 * kDenseUnshift<T>;
-            sum2 += d2;
         }
-    }
-#pragma unroll
-    for (int x = 16; x; x >>= 1) sum2 += __shfl_xor_sync(~0u, sum2, x);
-    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = sum2;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        float s = 0.f;
-        for (int x = 0; x < 8; ++x) s += part[x];
-        f.dlam_part[static_cast<long long>(bh) * f.row_tiles + t] = s;
     }
 }
 
@@ -772,11 +762,18 @@ __global__ void __launch_bounds__(256) dense_rows_kernel(const __grid_constant__
 // that is S^T), so W and dS, written by the thread of their row in 16 bits, are
 // the A operands of the accumulating products: W and dS_1 from tensor memory;
 // dS_2 from shared memory for keys, whose accumulators leave no columns for it.
-//   S_m = X_m x_m^T, dP = Y y^T      tcgen05 M = 128, N = 64, both from shared memory
+//   S_m = X_m x_m^T, dP = Y y^T      tcgen05 M = 128, N = 64
+// X and Y are A operands too: for queries they lie in tensor memory beside the
+// accumulators, and the products run at full rate (32 cycles a step of 16, where
+// both from shared memory, as for keys, take 48: its bandwidth is the bound there,
+// about 1800 cycles a tile with the loads, dS_2 and the row values).
 // S(i+1) is issued once both warpgroups have read S(i) into registers, and runs
 // while they form the weights of tile i: a warpgroup takes 32 of the 64 columns.
-// At N = 64 the S and dP products read shared memory at 1.5 times their math time.
-// Warps: w0 TMA producer, w1 MMA issuer, w4-11 two warpgroups.
+// The queries also sum P_2 (.) dP, which is delta_2 without the rounding of out2:
+// dlambda needs it, a sum of both signs in which those roundings would show.
+// Warps: w0 TMA producer, w1 issuer of S and dP, w2 issuer of the accumulating
+// products (an issue blocks until the tensor core takes it, so waits of the one
+// overlap issues of the other), w4-11 two warpgroups.
 template <int D>
 struct DenseBwdLayout {
     static constexpr int RBOX = 128 * 128, SBOX = 64 * 128;   // 64 columns of 128 / 64 rows
@@ -808,8 +805,8 @@ __device__ __forceinline__ void dense_bwd_cta(const DenseBwdMaps& tm, const Dens
                                               int item) {
     using L = DenseBwdLayout<D>;
     constexpr int NBOX = D / 64, SLOTS = L::SLOTS;
-    // tensor memory: S_1 | S_2 | dP | W (keys) or dS_2 | dS_1 | accumulators
-    constexpr uint32_t COL_DP = 128, COL_W = 192, COL_DS1 = 224, COL_ACC = 256;
+    // tensor memory: S_1 | S_2 | dP | W (keys) or dS_2 | dS_1 | accumulators (| queries: Q, dout)
+    constexpr uint32_t COL_DP = 128, COL_W = 192, COL_DS1 = 224, COL_ACC = 256, COL_X = 384, COL_Y = 448;
     // accumulators: keys dv first; then dk or dq: for d = 128 one of D columns (map m in its half), for d = 64
     // one for each map over all 64 columns of x, of which its half is the result (N = 64 either way)
     constexpr uint32_t COL_G = COL_ACC + (KEYS ? D : 0);
@@ -825,8 +822,9 @@ __device__ __forceinline__ void dense_bwd_cta(const DenseBwdMaps& tm, const Dens
     uint64_t* end_bar = p_free + 1;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(end_bar + 1);
     volatile int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
+    float* part = reinterpret_cast<float*>(smem + L::OFF_RING);         // [8] after the last product
 
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(~0u, tid >> 5, 0), lane = tid & 31;
     const int tiles = KEYS ? f.key_tiles : f.query_tiles, heads = KEYS ? a.Hk : a.H;
     // the tiles with the most visible partners first: early keys, late queries
     const int tile = KEYS ? item % tiles : tiles - 1 - item % tiles;
@@ -854,12 +852,12 @@ __device__ __forceinline__ void dense_bwd_cta(const DenseBwdMaps& tm, const Dens
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
         }
-        mbar_init(r_full, 1);
+        mbar_init(r_full, KEYS ? 1 : 8);
         mbar_init(s_full, 1);
         mbar_init(s_free, 8);
         mbar_init(p_full, 8);
         mbar_init(p_free, 1);
-        mbar_init(end_bar, 1);
+        mbar_init(end_bar, 2);
         *abort_flag = 0;
         fence_barrier_init();
     }
@@ -876,128 +874,150 @@ __device__ __forceinline__ void dense_bwd_cta(const DenseBwdMaps& tm, const Dens
         *abort_flag = 1;
         report(kStatusTimeout);
     };
-    auto stage = [&](int i) { return L::OFF_RING + (i % SLOTS) * L::STAGE; };
+    auto wait = [&](uint64_t* bar, uint32_t par) { return warp_wait(bar, par, abort_flag, lim); };
 
     if (warp == 0) {
-        if (lane == 0 && n > 0) {
-            // ================================================ producer
-            const CUtensorMap *mX = KEYS ? &tm.k : &tm.q, *mY = KEYS ? &tm.v : &tm.dout;
-            const CUtensorMap *mx = KEYS ? &tm.q : &tm.k, *my = KEYS ? &tm.dout : &tm.v;
-            const int Xh = hr * (KEYS ? f.k_h : f.q_h), Xb = b * (KEYS ? f.k_b : f.q_b);
-            const int Yh = hr * (KEYS ? f.v_h : f.do_h), Yb = b * (KEYS ? f.v_b : f.do_b);
+        // ==================================================== producer (the whole warp waits, one lane issues)
+        const bool leader = elect_one();
+        const CUtensorMap *mx = KEYS ? &tm.q : &tm.k, *my = KEYS ? &tm.dout : &tm.v;
+        if (KEYS && n > 0 && leader) {
             mbar_arrive_expect_tx(r_full, 2 * L::RES);
             for (int c = 0; c < NBOX; ++c)
                 for (int z = 0; z < 2; ++z) {
-                    tma_load_4d(smem + c * L::RBOX + z * L::SBOX, mX, r_full, c * 64, row0 + z * 64, Xh, Xb);
-                    tma_load_4d(smem + L::RES + c * L::RBOX + z * L::SBOX, mY, r_full, c * 64, row0 + z * 64, Yh, Yb);
+                    tma_load_4d(smem + c * L::RBOX + z * L::SBOX, &tm.k, r_full, c * 64, row0 + z * 64, hr * f.k_h,
+                                b * f.k_b);
+                    tma_load_4d(smem + L::RES + c * L::RBOX + z * L::SBOX, &tm.v, r_full, c * 64, row0 + z * 64,
+                                hr * f.v_h, b * f.v_b);
                 }
-            bool ok = true;
-            int i = 0;
-            for (; i < n; ++i) {
-                const int s = i % SLOTS, t = t0 + i % per, h = KEYS ? hr * a.G + i / per : hk;
-                if (i >= SLOTS && !mbar_wait(&empty[s], (i / SLOTS - 1) & 1, abort_flag, lim)) {
-                    ok = false;
-                    break;
-                }
-                unsigned char* st = smem + stage(i);
-                mbar_arrive_expect_tx(&full[s], 2 * L::STR + (KEYS ? kDenseRowFloats * 4 : 0));
-                const int xh = h * (KEYS ? f.q_h : f.k_h), xb = b * (KEYS ? f.q_b : f.k_b);
-                const int yh = h * (KEYS ? f.do_h : f.v_h), yb = b * (KEYS ? f.do_b : f.v_b);
+        }
+        __syncwarp();
+        const int xb = b * (KEYS ? f.q_b : f.k_b), yb = b * (KEYS ? f.do_b : f.v_b);
+        RingPos<SLOTS> rp{0, 1u};           // (phase of the wait for an empty slot: the first round passes)
+        bool ok = true;
+        int i = 0, t = t0, h = KEYS ? hr * a.G : hk;
+        for (; i < n; ++i) {
+            if (!(ok = wait(&empty[rp.slot], rp.phase))) break;
+            if (leader) {
+                unsigned char* st = smem + L::OFF_RING + rp.slot * L::STAGE;
+                uint64_t* bar = &full[rp.slot];
+                mbar_arrive_expect_tx(bar, 2 * L::STR + (KEYS ? kDenseRowFloats * 4 : 0));
+                const int xh = h * (KEYS ? f.q_h : f.k_h), yh = h * (KEYS ? f.do_h : f.v_h);
                 for (int c = 0; c < NBOX; ++c) {
-                    tma_load_4d(st + c * L::SBOX, mx, &full[s], c * 64, t * 64, xh, xb);
-                    tma_load_4d(st + L::STR + c * L::SBOX, my, &full[s], c * 64, t * 64, yh, yb);
+                    tma_load_4d(st + c * L::SBOX, mx, bar, c * 64, t * 64, xh, xb);
+                    tma_load_4d(st + L::STR + c * L::SBOX, my, bar, c * 64, t * 64, yh, yb);
                 }
                 if (KEYS)
                     bulk_load(st + 2 * L::STR,
                               f.rowdata + ((static_cast<long long>(b) * a.H + h) * f.row_tiles + t) * kDenseRowFloats,
-                              kDenseRowFloats * 4, &full[s]);
+                              kDenseRowFloats * 4, bar);
             }
-            if (!ok) fail();
-            mbar_wait(r_full, 0, abort_flag, drain_lim);    // every load has landed before the CTA exits
-            for (int y = max(0, i - SLOTS); y < i; ++y)
-                mbar_wait(&full[y % SLOTS], (y / SLOTS) & 1, abort_flag, drain_lim);
+            __syncwarp();
+            rp.step(1);
+            if (++t == t0 + per) t = t0, ++h;
         }
+        if (!ok) fail();
+        // every load has landed before the CTA exits
+        if (KEYS && n > 0) mbar_wait(r_full, 0, abort_flag, drain_lim);
+        for (int y = max(0, i - SLOTS); y < i; ++y) mbar_wait(&full[y % SLOTS], (y / SLOTS) & 1, abort_flag, drain_lim);
     } else if (warp == 1) {
-        if (lane == 0) {
-            // ================================================ MMA issuer
-            constexpr uint32_t ID_S = idesc_t<T>(128, 64, 0, 0), ID_V = idesc_t<T>(128, D, 0, 1),
-                               ID_G = idesc_t<T>(128, 64, 0, 1);
-            bool ok = n == 0 || mbar_wait(r_full, 0, abort_flag, lim);
-            for (int i = 0; ok && n > 0 && i <= n; ++i) {
-                if (i < n) {
-                    if (!mbar_wait(&full[i % SLOTS], (i / SLOTS) & 1, abort_flag, lim) ||
-                        (i > 0 && !mbar_wait(s_free, (i - 1) & 1, abort_flag, lim))) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint32_t x = sbase + stage(i), y = x + L::STR;
-                    constexpr int STEPS = D / 32;
+        // ==================================================== issuer of S and dP
+        constexpr uint32_t ID_S = idesc_t<T>(128, 64, 0, 0);
+        constexpr int STEPS = D / 32;
+        const bool leader = elect_one();
+        const uint64_t X0 = sdesc(sbase, 16, 1024, kSwizzle128B), Y0 = sdesc(sbase + L::RES, 16, 1024, kSwizzle128B),
+                       x0 = sdesc(sbase + L::OFF_RING, 16, 1024, kSwizzle128B);
+        RingPos<SLOTS> rp{0, 0u};
+        bool ok = n == 0 || wait(r_full, 0);
+        for (int i = 0; ok && i < n; ++i) {
+            if (!(ok = wait(&full[rp.slot], rp.phase))) break;
+            if (i > 0 && !(ok = wait(s_free, (i - 1) & 1))) break;
+            tc_fence_after();
+            if (leader) {
+                const uint64_t xd = x0 + rp.slot * (L::STAGE >> 4), yd = xd + (L::STR >> 4);
 #pragma unroll
-                    for (int kk = 0; kk < 2 * STEPS; ++kk)
-                        umma_f16_ss(tmem + (kk / STEPS) * 64,
-                                    sdesc(sbase + (kk >> 2) * L::RBOX + (kk & 3) * 32, 16, 1024, kSwizzle128B),
-                                    sdesc(x + (kk >> 2) * L::SBOX + (kk & 3) * 32, 16, 1024, kSwizzle128B), ID_S,
+                for (int kk = 0; kk < 2 * STEPS; ++kk) {
+                    const uint64_t bd = xd + (((kk >> 2) * L::SBOX + (kk & 3) * 32) >> 4);
+                    if (KEYS)
+                        umma_f16_ss(tmem + (kk / STEPS) * 64, X0 + (((kk >> 2) * L::RBOX + (kk & 3) * 32) >> 4), bd, ID_S,
                                     kk % STEPS ? 1u : 0u);
-#pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk)
-                        umma_f16_ss(tmem + COL_DP,
-                                    sdesc(sbase + L::RES + (kk >> 2) * L::RBOX + (kk & 3) * 32, 16, 1024, kSwizzle128B),
-                                    sdesc(y + (kk >> 2) * L::SBOX + (kk & 3) * 32, 16, 1024, kSwizzle128B), ID_S,
-                                    kk ? 1u : 0u);
-                    umma_commit(s_full);
+                    else
+                        umma_f16_ts(tmem + (kk / STEPS) * 64, tmem + COL_X + kk * 8, bd, ID_S, kk % STEPS ? 1u : 0u);
                 }
-                if (i > 0) {
-                    const int j = i - 1;
-                    if (!mbar_wait(p_full, j & 1, abort_flag, lim)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint32_t x = sbase + stage(j), y = x + L::STR;
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const uint32_t acc = j > 0 || k > 0 ? 1u : 0u;
-                        if (KEYS)
-                            umma_f16_ts(tmem + COL_ACC, tmem + COL_W + k * 8,
-                                        sdesc(y + k * 2048, L::SBOX, 1024, kSwizzle128B), ID_V, acc);
-                        umma_f16_ts(tmem + COL_G, tmem + COL_DS1 + k * 8,
-                                    sdesc(x + k * 2048, L::SBOX, 1024, kSwizzle128B), ID_G, acc);
-                        const uint64_t x2 = sdesc(x + (D == 128 ? L::SBOX : 0) + k * 2048, L::SBOX, 1024, kSwizzle128B);
-                        if (KEYS)
-                            umma_f16_ss(tmem + COL_G + 64, sdesc(sbase + L::OFF_DS2 + k * 32, 16, 1024, kSwizzle128B), x2,
-                                        ID_G, acc);
-                        else
-                            umma_f16_ts(tmem + COL_G + 64, tmem + COL_W + k * 8, x2, ID_G, acc);
-                    }
-                    umma_commit(p_free);
-                    umma_commit(&empty[j % SLOTS]);
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint64_t bd = yd + (((kk >> 2) * L::SBOX + (kk & 3) * 32) >> 4);
+                    if (KEYS)
+                        umma_f16_ss(tmem + COL_DP, Y0 + (((kk >> 2) * L::RBOX + (kk & 3) * 32) >> 4), bd, ID_S, kk ? 1u : 0u);
+                    else
+                        umma_f16_ts(tmem + COL_DP, tmem + COL_Y + kk * 8, bd, ID_S, kk ? 1u : 0u);
                 }
+                umma_commit(s_full);
             }
-            if (!ok) fail();
-            umma_commit(end_bar);          // also: every MMA has completed before tensor memory is released
-            mbar_wait(end_bar, 0, abort_flag, drain_lim);
+            __syncwarp();
+            rp.step(1);
         }
-    } else if (warp == 3) {
-        // dlambda_h = -sum over batch and queries of delta_2, in a fixed order: one CTA a head
-        if (!KEYS && b == 0 && tile == 0) {
-            double s = 0.0;
-            for (long long x = lane; x < static_cast<long long>(a.B) * f.row_tiles; x += 32)
-                s += f.dlam_part[(x / f.row_tiles * a.H + hr) * f.row_tiles + x % f.row_tiles];
+        if (!ok) fail();
+        if (leader) umma_commit(end_bar);      // also: every MMA has completed before tensor memory is released
+        mbar_wait(end_bar, 0, abort_flag, drain_lim);
+    } else if (warp == 2) {
+        // ==================================================== issuer of the accumulating products
+        constexpr uint32_t ID_V = idesc_t<T>(128, D, 0, 1), ID_G = idesc_t<T>(128, 64, 0, 1);
+        const bool leader = elect_one();
+        const uint64_t x0 = sdesc(sbase + L::OFF_RING, L::SBOX, 1024, kSwizzle128B),
+                       ds2 = sdesc(sbase + L::OFF_DS2, 16, 1024, kSwizzle128B);
+        RingPos<SLOTS> rp{0, 0u};
+        bool ok = true;
+        for (int i = 0; ok && i < n; ++i) {
+            if (!(ok = wait(&full[rp.slot], rp.phase)) || !(ok = wait(p_full, i & 1))) break;
+            tc_fence_after();
+            if (leader) {
+                const uint64_t xd = x0 + rp.slot * (L::STAGE >> 4), yd = xd + (L::STR >> 4);
 #pragma unroll
-            for (int x = 16; x; x >>= 1) s += __shfl_xor_sync(~0u, s, x);
-            if (lane == 0) static_cast<T*>(a.dlam)[hr] = from_f<T>(static_cast<float>(-s));
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t acc = i > 0 || k > 0 ? 1u : 0u;
+                    const uint64_t x1 = xd + ((k * 2048) >> 4), x2 = x1 + (D == 128 ? L::SBOX >> 4 : 0);
+                    if (KEYS) umma_f16_ts(tmem + COL_ACC, tmem + COL_W + k * 8, yd + ((k * 2048) >> 4), ID_V, acc);
+                    umma_f16_ts(tmem + COL_G, tmem + COL_DS1 + k * 8, x1, ID_G, acc);
+                    if (KEYS)
+                        umma_f16_ss(tmem + COL_G + 64, ds2 + ((k * 32) >> 4), x2, ID_G, acc);
+                    else
+                        umma_f16_ts(tmem + COL_G + 64, tmem + COL_W + k * 8, x2, ID_G, acc);
+                }
+                umma_commit(p_free);
+                umma_commit(&empty[rp.slot]);
+            }
+            __syncwarp();
+            rp.step(1);
         }
+        if (!ok) fail();
+        if (leader) umma_commit(end_bar);
+        mbar_wait(end_bar, 0, abort_flag, drain_lim);
     } else if (warp >= 4) {
         // ==================================================== warpgroups
         const int q4 = warp & 3, w = (warp - 4) >> 2, r = q4 * 32 + lane;
         const uint32_t tl = tmem + (static_cast<uint32_t>(q4 * 32) << 16);
-        auto wwait = [&](uint64_t* bar, uint32_t par) {
-            return warp_wait(bar, par, abort_flag, lim);
-        };
         const int row = row0 + r;
+        if (!KEYS && n > 0) {
+            // the resident rows to tensor memory: queries (w = 0) and dout (w = 1), zeros for padding
+            const T* src = static_cast<const T*>(w ? a.dout : a.q) +
+                           (row < qn ? (w ? a.dos.at(b, hr, row) : a.qs.at(b, hr, row)) : 0);
+#pragma unroll
+            for (int x = 0; x < NBOX; ++x) {
+                uint32_t v[32];
+#pragma unroll
+                for (int y = 0; y < 8; ++y) {
+                    const uint4 u = row < qn ? __ldg(reinterpret_cast<const uint4*>(src + x * 64) + y) : make_uint4(0, 0, 0, 0);
+                    v[4 * y] = u.x, v[4 * y + 1] = u.y, v[4 * y + 2] = u.z, v[4 * y + 3] = u.w;
+                }
+                tmem_st32(tl + (w ? COL_Y : COL_X) + x * 32, v);
+            }
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(r_full);
+        }
         const float c = a.scale_log2;
-        const uint64_t c2 = f2pack(c, c), un2 = f2pack(kDenseUnshift<T>, kDenseUnshift<T>);
+        const uint64_t c2 = f2pack(c, c), un2 = f2pack(kDenseUnshift<T>, kDenseUnshift<T>), neg2 = f2pack(-1.f, -1.f);
         uint64_t nl1 = 0, nl2 = 0, nd1 = 0, nd2 = 0;          // queries: this row's values
         if (!KEYS && n > 0) {
             const int t = row >> 6;
@@ -1009,17 +1029,15 @@ __device__ __forceinline__ void dense_bwd_cta(const DenseBwdMaps& tm, const Dens
             nl1 = f2pack(v0, v0), nl2 = f2pack(v1, v1), nd1 = f2pack(v2, v2), nd2 = f2pack(v3, v3);
         }
         const int own = dense_own(row, qn, kn, a.causal);     // queries
-        float lam = KEYS ? 0.f : to_f<T>(static_cast<const T*>(a.lam)[hr]);
+        const T* lams = static_cast<const T*>(a.lam) + (KEYS ? hr * a.G : hr);
+        float lam = to_f<T>(lams[0]);
+        uint64_t delta2 = 0;                                  // queries: the sum of P_2 dP, scaled as P
+        RingPos<SLOTS> rp{0, 0u};
         bool ok = true;
+        int t = t0;
         for (int i = 0; i < n; ++i) {
-            const int t = t0 + i % per, base = t * 64 + w * 32;
-            if (KEYS && i % per == 0) lam = to_f<T>(static_cast<const T*>(a.lam)[hr * a.G + i / per]);
-            const uint64_t lam2 = f2pack(lam, lam), neg2 = f2pack(-1.f, -1.f);
             // (keys: this thread reads the tile's row values itself, so it also waits for their load)
-            if (!wwait(s_full, i & 1) || (KEYS && !wwait(&full[i % SLOTS], (i / SLOTS) & 1))) {
-                ok = false;
-                break;
-            }
+            if (!(ok = wait(s_full, i & 1)) || (KEYS && !(ok = wait(&full[rp.slot], rp.phase)))) break;
             tc_fence_after();
             uint32_t s1[32], s2[32], dp[32];
             tmem_ld32(tl + w * 32, s1);
@@ -1029,6 +1047,7 @@ __device__ __forceinline__ void dense_bwd_cta(const DenseBwdMaps& tm, const Dens
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(s_free);
+            const int base = t * 64 + w * 32;
             // columns [lo, hi) count; the others may hold anything
             const int lo = KEYS && a.causal ? row - off - base : 0;
             const int hi = KEYS ? (t == dirty ? qn - base : 32) : own - base;
@@ -1040,7 +1059,8 @@ __device__ __forceinline__ void dense_bwd_cta(const DenseBwdMaps& tm, const Dens
                         dp[x] = 0u;
                     }
             }
-            unsigned char* st = smem + stage(i);
+            const uint64_t lam2 = f2pack(lam, lam);
+            unsigned char* st = smem + L::OFF_RING + rp.slot * L::STAGE;
             const float* rd = reinterpret_cast<const float*>(st + 2 * L::STR) + w * 32;
             uint32_t ww[16], d1[16], d2[16];
 #pragma unroll
@@ -1060,11 +1080,13 @@ __device__ __forceinline__ void dense_bwd_cta(const DenseBwdMaps& tm, const Dens
                 for (int z = 0; z < 2; ++z) {
                     const int y = 2 * x + z, k = 2 * y;
                     float u, v;
-                    const uint64_t x1 = ffma2(f2pack(__uint_as_float(s1[k]), __uint_as_float(s1[k + 1])), c2, l1[z]);
-                    const uint64_t p1 = exp2_2(x1);
-                    const uint64_t x2 = ffma2(f2pack(__uint_as_float(s2[k]), __uint_as_float(s2[k + 1])), c2, l2[z]);
-                    const uint64_t p2 = fmul2(exp2_2(x2), lam2);
+                    const uint64_t p1 =
+                        exp2_2(ffma2(f2pack(__uint_as_float(s1[k]), __uint_as_float(s1[k + 1])), c2, l1[z]));
+                    const uint64_t q2 =
+                        exp2_2(ffma2(f2pack(__uint_as_float(s2[k]), __uint_as_float(s2[k + 1])), c2, l2[z]));
                     const uint64_t g = f2pack(__uint_as_float(dp[k]), __uint_as_float(dp[k + 1]));
+                    if (!KEYS) delta2 = ffma2(q2, g, delta2);
+                    const uint64_t p2 = fmul2(q2, lam2);
                     f2unpack(fmul2(p1, ffma2(g, un2, e1[z])), u, v);
                     d1[y] = pack2<T>(u, v);
                     f2unpack(fmul2(p2, ffma2(g, un2, e2[z])), u, v);
@@ -1077,10 +1099,7 @@ __device__ __forceinline__ void dense_bwd_cta(const DenseBwdMaps& tm, const Dens
             }
             // the last tile's products have read W and dS
             if (i > 0) {
-                if (!wwait(p_free, (i - 1) & 1)) {
-                    ok = false;
-                    break;
-                }
+                if (!(ok = wait(p_free, (i - 1) & 1))) break;
                 tc_fence_after();
             }
             tmem_st16(tl + COL_DS1 + w * 16, d1);
@@ -1094,6 +1113,7 @@ __device__ __forceinline__ void dense_bwd_cta(const DenseBwdMaps& tm, const Dens
                 tmem_st16(tl + COL_W + w * 16, d2);
             }
             if (t == dirty) {      // rows past the length to zero: they are B operands of the products below
+                if (!KEYS && !(ok = wait(&full[rp.slot], rp.phase))) break;
                 const int rz = slen % 64;
                 for (int y = w * 128 + r; y < (64 - rz) * 8; y += 256)
 #pragma unroll
@@ -1105,9 +1125,14 @@ __device__ __forceinline__ void dense_bwd_cta(const DenseBwdMaps& tm, const Dens
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(p_full);
+            rp.step(1);
+            if (++t == t0 + per) {
+                t = t0;
+                if (KEYS && i + 1 < n) lam = to_f<T>(*++lams);
+            }
         }
         if (!ok) fail();
-        ok = wwait(end_bar, 0) && ok;
+        ok = wait(end_bar, 0) && ok;
         tc_fence_after();
         // ---------------------------------------------------- results: keys dv (w = 0) and dk (w = 1), queries halves of dq
         const bool in = row < (KEYS ? a.Nk : a.Nq), some = n > 0 && row < (KEYS ? kn : qn);
@@ -1132,6 +1157,37 @@ __device__ __forceinline__ void dense_bwd_cta(const DenseBwdMaps& tm, const Dens
                                     : 0u;
                     reinterpret_cast<uint4*>(dst + x)[y] = make_uint4(u[0], u[1], u[2], u[3]);
                 }
+        }
+        if (!KEYS) {
+            // delta_2 of the CTA's rows, its place among the head's, and the head's sum from whoever is last: the
+            // places are added in one order
+            float u, v;
+            f2unpack(delta2, u, v);
+            float s = some ? (u + v) * kDenseUnshift<T> : 0.f;
+#pragma unroll
+            for (int x = 16; x; x >>= 1) s += __shfl_xor_sync(~0u, s, x);
+            if (lane == 0) part[warp - 4] = s;
+            named_bar(1, 256);
+            if (warp == 4) {
+                const long long places = static_cast<long long>(a.B) * f.query_tiles;
+                float* mine = f.dlam_part + hr * places;
+                unsigned before = 0u;
+                if (lane == 0) {
+                    float sum = 0.f;
+                    for (int x = 0; x < 8; ++x) sum += part[x];
+                    mine[static_cast<long long>(b) * f.query_tiles + tile] = sum;
+                    __threadfence();
+                    before = atomicAdd(&f.dlam_done[hr], 1u);
+                }
+                if (__shfl_sync(~0u, before, 0) == places - 1) {
+                    __threadfence();
+                    double sum = 0.0;
+                    for (long long x = lane; x < places; x += 32) sum += __ldcg(mine + x);
+#pragma unroll
+                    for (int x = 16; x; x >>= 1) sum += __shfl_xor_sync(~0u, sum, x);
+                    if (lane == 0) static_cast<T*>(a.dlam)[hr] = from_f<T>(static_cast<float>(-sum));
+                }
+            }
         }
     }
     tc_fence_before();

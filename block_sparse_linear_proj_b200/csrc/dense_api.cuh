@@ -93,7 +93,7 @@ DensePlan dense_plan(const sla_dense_params_t* p) {
 }
 
 struct DenseWs {
-    size_t rowdata, dlam_part, opart, lpart, total;
+    size_t rowdata, dlam_part, dlam_done, opart, lpart, total;
 };
 
 DenseWs dense_layout(const sla_dense_params_t* p) {
@@ -113,7 +113,8 @@ DenseWs dense_layout(const sla_dense_params_t* p) {
     if (p->differential) {
         const size_t tiles = static_cast<size_t>(p->B) * p->H * ((p->Nq + sla::kDenseRowTile - 1) / sla::kDenseRowTile);
         w.rowdata = take(tiles * sla::kDenseRowFloats * 4);
-        w.dlam_part = take(tiles * 4);
+        w.dlam_part = take(tiles * 4);         // (a place for each 128 queries; one for each 64 are enough)
+        w.dlam_done = take(static_cast<size_t>(p->H) * 4);
     }
     w.total = std::max<size_t>(std::max(w.total, off), kAlign);
     return w;
@@ -215,7 +216,7 @@ sla_status_t dense_bwd(const sla_dense_params_t* p, const sla::DenseArgs& a, voi
     f.query_tiles = (p->Nq + 127) / 128;
     f.row_tiles = (p->Nq + sla::kDenseRowTile - 1) / sla::kDenseRowTile;
     f.key_items = p->B * p->Hk * f.key_tiles;
-    f.rowdata = at<float>(ws, w.rowdata), f.dlam_part = at<float>(ws, w.dlam_part);
+    f.rowdata = at<float>(ws, w.rowdata), f.dlam_part = at<float>(ws, w.dlam_part), f.dlam_done = at<unsigned>(ws, w.dlam_done);
     f.wait_ns = wait_limit_ns();
     sla::DenseBwdMaps tm{};
     constexpr bool half = std::is_same<T, __half>::value;

@@ -6,7 +6,8 @@ rounds, in io_dtype:
   forward   the softmax weights (relative to their running maximum) and the
             results:  |d out| <= u sum_m |w_m| P_m |v| + u |out|,  w = (1, lambda)
   backward  W = P_1 - lambda P_2, dS_m and the results; and it reads the rounded
-            out and out2, which moves delta_m by at most |dout| . (their errors).
+            out and out2, which moves delta_m by at most |dout| . (their errors);
+            dlambda comes from the unrounded weights.
 Everything else is fp32: sums of up to thousands of terms, exponentials and
 log-sum-exps, taken as SLACK relative to the sums of magnitudes (2^-13, an
 eighth of an fp16 rounding is 2^-14; logits of magnitude 30 alone put
@@ -112,7 +113,7 @@ def dense(q, k, v, lam=None, kp=None, vp=None, q_len=None, kv_len=None, causal=F
             r["dk"][b, hk, :m] += torch.cat(dk, -1)
             tol["dk"][b, hk, :m] += torch.cat(tk, -1)
             r["dlam"][h] -= d2.sum()
-            tol["dlam"][h] += e2.sum()
+            tol["dlam"][h] += SLACK * (p2 * gv).sum()
     for n in ("dq", "dk", "dv", "dlam"):
         if n in r:
             tol[n] += u * (r[n].abs() + tol[n]) + t0 + 1e-30
