@@ -281,7 +281,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
     const bool every = DIFF || two;                 // each stream takes every tile
     const int lead = every ? 1 : 2;
 
-    if (warp < 4) reg_dec<56>();
+    if (warp < 4) reg_dec<72>();
     if (warp == 0) {
         // ==================================================== producer (the whole warp waits, one lane issues)
         const bool leader = elect_one();
@@ -380,7 +380,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
         if (leader) umma_commit(o_full);   // also: every MMA has completed before tensor memory is released
         mbar_wait(o_full, 0, abort_flag, drain_lim);
     } else if (warp >= 4) {
-        reg_inc<224>();
+        reg_inc<216>();
         // ==================================================== streams
         const int q4 = warp & 3, s = (warp - 4) >> 2, r = q4 * 32 + lane;
         const uint32_t tl = tmem + (static_cast<uint32_t>(q4 * 32) << 16);
@@ -1017,7 +1017,7 @@ __device__ __forceinline__ void dense_bwd_cta(const DenseBwdMaps& tm, const Dens
             if (lane == 0) mbar_arrive(r_full);
         }
         const float c = a.scale_log2;
-        const uint64_t c2 = f2pack(c, c), un2 = f2pack(kDenseUnshift<T>, kDenseUnshift<T>), neg2 = f2pack(-1.f, -1.f);
+        const uint64_t c2 = f2pack(c, c), un2 = f2pack(kDenseUnshift<T>, kDenseUnshift<T>);
         uint64_t nl1 = 0, nl2 = 0, nd1 = 0, nd2 = 0;          // queries: this row's values
         if (!KEYS && n > 0) {
             const int t = row >> 6;
@@ -1037,16 +1037,19 @@ __device__ __forceinline__ void dense_bwd_cta(const DenseBwdMaps& tm, const Dens
         int t = t0;
         for (int i = 0; i < n; ++i) {
             // (keys: this thread reads the tile's row values itself, so it also waits for their load)
-            if (!(ok = wait(s_full, i & 1)) || (KEYS && !(ok = wait(&full[rp.slot], rp.phase)))) break;
-            tc_fence_after();
+            ok = ok && wait(s_full, i & 1) && (!KEYS || wait(&full[rp.slot], rp.phase));
             uint32_t s1[32], s2[32], dp[32];
-            tmem_ld32(tl + w * 32, s1);
-            tmem_ld32(tl + 64 + w * 32, s2);
-            tmem_ld32(tl + COL_DP + w * 32, dp);
-            tmem_ld_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(s_free);
+            if (ok) {
+                tc_fence_after();
+                tmem_ld32(tl + w * 32, s1);
+                tmem_ld32(tl + 64 + w * 32, s2);
+                tmem_ld32(tl + COL_DP + w * 32, dp);
+                tmem_ld_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(s_free);
+            }
+            if (!ok) break;
             const int base = t * 64 + w * 32;
             // columns [lo, hi) count; the others may hold anything
             const int lo = KEYS && a.causal ? row - off - base : 0;
@@ -1059,7 +1062,7 @@ __device__ __forceinline__ void dense_bwd_cta(const DenseBwdMaps& tm, const Dens
                         dp[x] = 0u;
                     }
             }
-            const uint64_t lam2 = f2pack(lam, lam);
+            const uint64_t nlam2 = f2pack(-lam, -lam);
             unsigned char* st = smem + L::OFF_RING + rp.slot * L::STAGE;
             const float* rd = reinterpret_cast<const float*>(st + 2 * L::STR) + w * 32;
             uint32_t ww[16], d1[16], d2[16];
@@ -1080,20 +1083,22 @@ __device__ __forceinline__ void dense_bwd_cta(const DenseBwdMaps& tm, const Dens
                 for (int z = 0; z < 2; ++z) {
                     const int y = 2 * x + z, k = 2 * y;
                     float u, v;
-                    const uint64_t p1 =
-                        exp2_2(ffma2(f2pack(__uint_as_float(s1[k]), __uint_as_float(s1[k + 1])), c2, l1[z]));
-                    const uint64_t q2 =
-                        exp2_2(ffma2(f2pack(__uint_as_float(s2[k]), __uint_as_float(s2[k + 1])), c2, l2[z]));
+                    const uint64_t x1 = ffma2(f2pack(__uint_as_float(s1[k]), __uint_as_float(s1[k + 1])), c2, l1[z]);
+                    const uint64_t x2 = ffma2(f2pack(__uint_as_float(s2[k]), __uint_as_float(s2[k + 1])), c2, l2[z]);
+                    const uint64_t p1 = exp2_2(x1), q2 = exp2_2(x2);
                     const uint64_t g = f2pack(__uint_as_float(dp[k]), __uint_as_float(dp[k + 1]));
                     if (!KEYS) delta2 = ffma2(q2, g, delta2);
-                    const uint64_t p2 = fmul2(q2, lam2);
                     f2unpack(fmul2(p1, ffma2(g, un2, e1[z])), u, v);
                     d1[y] = pack2<T>(u, v);
-                    f2unpack(fmul2(p2, ffma2(g, un2, e2[z])), u, v);
-                    d2[y] = pack2<T>(-u, -v);
                     if (KEYS) {
-                        f2unpack(ffma2(p2, neg2, p1), u, v);
+                        const uint64_t p2 = fmul2(q2, nlam2);          // -lambda P_2
+                        f2unpack(fmul2(p2, ffma2(g, un2, e2[z])), u, v);
+                        d2[y] = pack2<T>(u, v);
+                        f2unpack(fadd2(p1, p2), u, v);
                         ww[y] = pack2<T>(u, v);
+                    } else {                                           // (dq_2 takes -lambda in the end)
+                        f2unpack(fmul2(q2, ffma2(g, un2, e2[z])), u, v);
+                        d2[y] = pack2<T>(u, v);
                     }
                 }
             }
@@ -1138,7 +1143,8 @@ __device__ __forceinline__ void dense_bwd_cta(const DenseBwdMaps& tm, const Dens
         const bool in = row < (KEYS ? a.Nk : a.Nq), some = n > 0 && row < (KEYS ? kn : qn);
         const int x0 = KEYS ? 0 : w * (D / 2), x1 = KEYS ? D : x0 + D / 2;
         const bool is_v = KEYS && w == 0;
-        const float k = is_v ? kDenseUnshift<T> : a.scale;
+        // (w = 1 of the queries holds the second map's half)
+        const float k = is_v ? kDenseUnshift<T> : !KEYS && w == 1 ? -lam * a.scale : a.scale;
         T* dst = static_cast<T*>(KEYS ? (is_v ? a.dv : a.dk) : a.dq) +
                  (in ? (KEYS ? (is_v ? a.dvs.at(b, hr, row) : a.dks.at(b, hr, row)) : a.dqs.at(b, hr, row)) : 0);
 #pragma unroll 1
