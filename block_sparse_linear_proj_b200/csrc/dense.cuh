@@ -385,33 +385,13 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
         const int q4 = warp & 3, s = (warp - 4) >> 2, r = q4 * 32 + lane;
         const uint32_t tl = tmem + (static_cast<uint32_t>(q4 * 32) << 16);
         auto wwait = [&](uint64_t* bar, uint32_t par) { return warp_wait(bar, par, abort_flag, lim); };
-        // the query rows, 16 bytes a thread: zeros where there is no query
-        if (n > 0) {
-            constexpr int CH = D / 8;                           // 16-byte chunks a row
-            const int nrow = two ? 256 : 128;
-            for (int x = tid - 128; x < nrow * CH; x += 256) {
-                const int rr = x / CH, c = x % CH, gr = row0 + rr;
-                uint4 val = make_uint4(0, 0, 0, 0);
-                if (gr < rows) {
-                    const int b = gathered ? gr / per_seq : b0, lr = gathered ? gr % per_seq : gr;
-                    const int i = lr / a.G, g = lr % a.G;
-                    if (i < (gathered ? dense_len(a.q_len, b, a.Nq) : qn0))
-                        val = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) +
-                                                                   a.qs.at(b, hk * a.G + g, i) + c * 8));
-                }
-                *reinterpret_cast<uint4*>(smem + (rr >> 7) * L::QTILE + (c >> 3) * L::QBOX + sw128(rr & 127, c & 7)) = val;
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(q_full);
-        }
-        // this thread's row (asked for again after the loop, which has few registers left)
+        // a row of the CTA's (this thread's is asked for again after the loop, which has few registers left)
         struct Row {
             int b, lr, qi, h;
             bool in, real;
         };
         auto row_of = [&](int rr) {
-            const int gr = row0 + (two ? s * 128 : 0) + rr;
+            const int gr = row0 + rr;
             Row x;
             x.in = gr < rows;
             x.b = gathered ? (x.in ? gr / per_seq : 0) : b0;
@@ -421,7 +401,31 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
             x.real = x.in && x.qi < (gathered ? dense_len(a.q_len, x.b, a.Nq) : qn0);
             return x;
         };
-        const int own_r = gathered ? 0 : dense_own(row_of(r).qi, qn0, kn0, a.causal);
+        const int my_row = (two ? s * 128 : 0) + r;
+        if (n > 0) {
+            // the query rows, a thread a row (or half of one): zeros where there is no query.  All of a thread's loads
+            // are in flight at once (one chunk of a row after the other took up to 11 us for 256 gathered rows)
+            constexpr int CH = D / 16;                          // 16-byte chunks of half a row
+            const int rr = two ? tid - 128 : (tid - 128) & 127;
+            const Row x = row_of(rr);
+            const uint4* src = reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) +
+                                                              (x.real ? a.qs.at(x.b, x.h, x.qi) : 0));
+#pragma unroll
+            for (int z = 0; z < 2; ++z) {
+                if (!two && z != s) continue;
+                uint4 v[CH];
+#pragma unroll
+                for (int c = 0; c < CH; ++c) v[c] = x.real ? __ldg(src + z * CH + c) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                for (int c = 0; c < CH; ++c)
+                    *reinterpret_cast<uint4*>(smem + (rr >> 7) * L::QTILE + ((z * CH + c) >> 3) * L::QBOX +
+                                              sw128(rr & 127, (z * CH + c) & 7)) = v[c];
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(q_full);
+        }
+        const int own_r = gathered ? 0 : dense_own(row_of(my_row).qi, qn0, kn0, a.causal);
         const float c = a.scale_log2, grow = 8.f / c;
         float m = -INFINITY, l = 0.f;                           // reference maximum (raw logits), sum
         bool ok = true;
@@ -516,7 +520,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
         // ---------------------------------------------------- results
         ok = wwait(o_full, 0) && ok;
         tc_fence_after();
-        int again = r;
+        int again = my_row;
         asm volatile("" : "+r"(again));
         const Row me = row_of(again);
         const int b = me.b, lr = me.lr, qi = me.qi, h = me.h;
@@ -535,6 +539,23 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
                 a.lse[((static_cast<long long>(b) * a.H + h) * M + (DIFF ? s : 0)) * a.Nq + qi] =
                     lse2 * 0.6931471805599453f;
         }
+        // Rows go out through shared memory, so that a warp writes whole rows: put() stages 16 bytes of this thread's
+        // row, flush() writes the warp's 32 rows to their places (null: none).
+        unsigned char* stage = smem + L::OFF_RING + 1024 + (warp - 4) * (32 * D * 4);
+        auto put = [&](int at, int row_bytes, int chunk, uint4 v) {
+            *reinterpret_cast<uint4*>(stage + at + lane * row_bytes + ((chunk ^ (lane & 3)) << 4)) = v;
+        };
+        auto flush = [&](int at, auto row_bytes, void* dst) {
+            constexpr int RB = decltype(row_bytes)::value, LANES = RB / 16;
+            const int c = lane % LANES;
+#pragma unroll 4
+            for (int y = 0; y < LANES; ++y) {
+                const int rr = y * (32 / LANES) + lane / LANES;
+                char* to = reinterpret_cast<char*>(__shfl_sync(~0u, reinterpret_cast<unsigned long long>(dst), rr));
+                const uint4 v = *reinterpret_cast<const uint4*>(stage + at + rr * RB + ((c ^ (rr & 3)) << 4));
+                if (to) reinterpret_cast<uint4*>(to)[c] = v;
+            }
+        };
         if (DIFF && f.direct) {
             // both maps' sums of this row (every product and load is complete: the ring is free), then half of its
             // columns a warpgroup
@@ -543,13 +564,12 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
             const float l1 = xl[r], l2 = xl[128 + r];
             const float i1 = l1 > 0.f ? 1.f / l1 : 0.f, i2 = l2 > 0.f ? 1.f / l2 : 0.f;
             const float lam = to_f<T>(static_cast<const T*>(a.lam)[h]);
-            T* op = static_cast<T*>(a.out) + (in ? a.os.at(b, h, qi) : 0);
-            T* o2p = a.out2 ? static_cast<T*>(a.out2) + ((static_cast<long long>(b) * a.H + h) * a.Nq + qi) * D : nullptr;
+            const bool second = a.out2 != nullptr;
 #pragma unroll 1
-            for (int x = s * (D / 2); x < (s + 1) * (D / 2); x += 16) {
+            for (int x = 0; x < D / 2; x += 16) {
                 uint32_t o1[16], o2[16], w1[8], w2[8];
-                tmem_ld16(tl + COL_O + x, o1);
-                tmem_ld16(tl + COL_O + D + x, o2);
+                tmem_ld16(tl + COL_O + s * (D / 2) + x, o1);
+                tmem_ld16(tl + COL_O + D + s * (D / 2) + x, o2);
                 tmem_ld_wait();
 #pragma unroll
                 for (int y = 0; y < 8; ++y) {
@@ -560,21 +580,21 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
                     w1[y] = pack2<T>(fmaf(-lam, a0, b0_), fmaf(-lam, a1, b1_));
                     w2[y] = pack2<T>(a0, a1);
                 }
-                if (in && ok) {
 #pragma unroll
-                    for (int y = 0; y < 2; ++y) {
-                        reinterpret_cast<uint4*>(op + x)[y] = make_uint4(w1[4 * y], w1[4 * y + 1], w1[4 * y + 2], w1[4 * y + 3]);
-                        if (o2p)
-                            reinterpret_cast<uint4*>(o2p + x)[y] =
-                                make_uint4(w2[4 * y], w2[4 * y + 1], w2[4 * y + 2], w2[4 * y + 3]);
-                    }
+                for (int y = 0; y < 2; ++y) {
+                    put(0, D, x / 8 + y, make_uint4(w1[4 * y], w1[4 * y + 1], w1[4 * y + 2], w1[4 * y + 3]));
+                    if (second) put(32 * D, D, x / 8 + y, make_uint4(w2[4 * y], w2[4 * y + 1], w2[4 * y + 2], w2[4 * y + 3]));
                 }
             }
+            __syncwarp();
+            const bool write = in && ok;
+            flush(0, std::integral_constant<int, D>{}, write ? static_cast<T*>(a.out) + a.os.at(b, h, qi) + s * (D / 2) : nullptr);
+            if (second)
+                flush(32 * D, std::integral_constant<int, D>{},
+                      write ? static_cast<T*>(a.out2) + ((static_cast<long long>(b) * a.H + h) * a.Nq + qi) * D + s * (D / 2)
+                            : nullptr);
         } else {
             const float inv = l > 0.f ? 1.f / l : 0.f;
-            T* op = static_cast<T*>(a.out) + (in ? a.os.at(b, h, qi) : 0);
-            float* pp = f.direct ? nullptr : f.opart + (in ? part : 0) * D;
-            const bool write = in && ok && (f.direct || l > 0.f);
 #pragma unroll 1
             for (int x = 0; x < D; x += 16) {
                 uint32_t o[16];
@@ -582,7 +602,6 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
                 tmem_ld_wait();
 #pragma unroll
                 for (int y = 0; y < 16; ++y) o[y] = l > 0.f ? __float_as_uint(__uint_as_float(o[y]) * inv) : 0u;
-                if (!write) continue;
                 if (f.direct) {
 #pragma unroll
                     for (int y = 0; y < 2; ++y) {
@@ -590,14 +609,19 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
 #pragma unroll
                         for (int z = 0; z < 4; ++z)
                             w[z] = pack2<T>(__uint_as_float(o[8 * y + 2 * z]), __uint_as_float(o[8 * y + 2 * z + 1]));
-                        reinterpret_cast<uint4*>(op + x)[y] = make_uint4(w[0], w[1], w[2], w[3]);
+                        put(0, 2 * D, x / 8 + y, make_uint4(w[0], w[1], w[2], w[3]));
                     }
                 } else {
 #pragma unroll
                     for (int y = 0; y < 4; ++y)
-                        reinterpret_cast<uint4*>(pp + x)[y] = make_uint4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
+                        put(0, 4 * D, x / 4 + y, make_uint4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]));
                 }
             }
+            __syncwarp();
+            if (f.direct)
+                flush(0, std::integral_constant<int, 2 * D>{}, in && ok ? static_cast<T*>(a.out) + a.os.at(b, h, qi) : nullptr);
+            else      // (a row that saw nothing has no part)
+                flush(0, std::integral_constant<int, 4 * D>{}, in && ok && l > 0.f ? f.opart + part * D : nullptr);
         }
     }
     tc_fence_before();

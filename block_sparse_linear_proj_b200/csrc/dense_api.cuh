@@ -77,10 +77,11 @@ DensePlan dense_plan(const sla_dense_params_t* p) {
         cg = static_cast<long long>(p->Hk) * x.tiles_g;
         work += cg * nP;
     }
-    // a range of key tiles a CTA so that all of them run at once, four tiles at least (a CTA's start and
-    // the join cost about as much as that many)
-    const long long share = std::max<long long>(4, cdiv(work, SMS));
-    x.splits_b = static_cast<int>(cb >= SMS ? 1 : std::max<long long>(1, std::min(cdiv(tb, share), SMS / cb)));
+    // A range of key tiles a CTA: where there are few CTAs, three ranges for each SM's share, so that sequences of
+    // different lengths even out, but eight tiles (two where that would leave SMs without a CTA): a CTA's start and the
+    // join cost as much as about that many.
+    const long long share = std::max<long long>(work >= 8 * SMS ? 8 : 2, cdiv(work, 3 * SMS));
+    x.splits_b = static_cast<int>(cb >= 3 * SMS ? 1 : std::max<long long>(1, std::min(cdiv(tb, share), 3 * SMS / cb)));
     x.splits_g = gather ? static_cast<int>(std::max<long long>(1, cdiv(nP, share))) : 0;
     // a stream of every second tile is a part of its own
     x.slots_b = x.splits_b * (!diff && !x.two_b ? 2 : 1);
@@ -118,6 +119,28 @@ DenseWs dense_layout(const sla_dense_params_t* p) {
     }
     w.total = std::max<size_t>(std::max(w.total, off), kAlign);
     return w;
+}
+
+// Shared memory above the default is asked for once a kernel and device, and again if a launch says it is not there
+// (a context that was reset).
+template <typename K, typename... A>
+sla_status_t dense_launch(K* kern, std::atomic<unsigned long long>& asked, unsigned grid, int smem, cudaStream_t st,
+                          const A&... args) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return SLA_ERR_CUDA;
+    const unsigned long long bit = 1ull << (dev & 63);
+    for (int tries = 0; tries < 2; ++tries) {
+        const bool fresh = tries || dev > 63 || !(asked.load(std::memory_order_relaxed) & bit);
+        if (fresh) {
+            if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+                return SLA_ERR_CUDA;
+            asked.fetch_or(bit, std::memory_order_relaxed);
+        }
+        kern<<<grid, sla::kDenseThreads, smem, st>>>(args...);
+        if (cudaGetLastError() == cudaSuccess) return SLA_OK;
+        if (fresh) break;
+    }
+    return SLA_ERR_CUDA;
 }
 
 // 4-D map over a [B, Hk, N, d] tensor of 16-bit values, box 64 x tokens (128-byte swizzle).  A dimension of
@@ -184,12 +207,12 @@ sla_status_t dense_fwd_t(const sla_dense_params_t* p, const sla::DenseArgs& a, v
     if (p->P && (!dense_map(&tm.kp, a.kp, a.kps, 1, p->Hk, p->P, D, half) ||
                  !dense_map(&tm.vp, a.vp, a.vps, 1, p->Hk, p->P, D, half)))
         return SLA_ERR_CUDA;
-    auto kern = sla::dense_fwd_kernel<D, T, DIFF>;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM) != cudaSuccess)
-        return SLA_ERR_CUDA;
+    static std::atomic<unsigned long long> asked{0};
     {
         Span sp(SLA_KERNEL_DENSE, st);
-        kern<<<x.items, sla::kDenseThreads, L::SMEM, st>>>(tm, f);
+        const sla_status_t s = dense_launch(sla::dense_fwd_kernel<D, T, DIFF>, asked, static_cast<unsigned>(x.items),
+                                            L::SMEM, st, tm, f);
+        if (s != SLA_OK) return s;
     }
     if (!x.direct) {
         Span sp(SLA_KERNEL_DENSE, st);
@@ -225,16 +248,17 @@ sla_status_t dense_bwd(const sla_dense_params_t* p, const sla::DenseArgs& a, voi
         (p->Nk && (!dense_map(&tm.k, a.k, a.ks, p->B, p->Hk, p->Nk, D, half, 64) ||
                    !dense_map(&tm.v, a.v, a.vs, p->B, p->Hk, p->Nk, D, half, 64))))
         return SLA_ERR_CUDA;
-    auto kern = sla::dense_bwd_kernel<D, T>;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM) != cudaSuccess)
-        return SLA_ERR_CUDA;
+    static std::atomic<unsigned long long> asked{0};
     {
         Span sp(SLA_KERNEL_DENSE_BWD, st);
         sla::dense_rows_kernel<D, T><<<p->B * p->H * f.row_tiles, 256, 0, st>>>(f);
     }
     {
         Span sp(SLA_KERNEL_DENSE_BWD, st);
-        kern<<<f.key_items + p->B * p->H * f.query_tiles, sla::kDenseThreads, L::SMEM, st>>>(tm, f);
+        const sla_status_t s = dense_launch(sla::dense_bwd_kernel<D, T>, asked,
+                                            static_cast<unsigned>(f.key_items + p->B * p->H * f.query_tiles), L::SMEM, st,
+                                            tm, f);
+        if (s != SLA_OK) return s;
     }
     return launch_status();
 }

@@ -424,6 +424,17 @@ class _DenseArgs:
     def __init__(self, p):
         self.dtype, self.dev, self.strides = io_torch_dtype(p), torch.cuda.current_device(), []
 
+    def stream(self, stream):
+        # (the raw handle: a Stream object costs as much as the rest of the call)
+        if stream is None:
+            return torch._C._cuda_getCurrentRawStream(self.dev)
+        return _stream(stream)
+
+    def workspace(self, ws):
+        if ws.get_device() != self.dev or not ws.is_contiguous():
+            _ptr(ws)       # raises
+        return ws.data_ptr(), _nbytes(ws)
+
     def _addr(self, t, dtype, shape, name):
         if t.dtype != dtype:
             raise TypeError("%s: expected %s, got %s" % (name, dtype, t.dtype))
@@ -477,7 +488,7 @@ def sla_diff_forward(p, q, k, v, lam, out, ws, lse=None, out2=None, q_len=None, 
             a.dense(lam, a.dtype, (p.H,), "lam"), a.dense(q_len, torch.int32, (p.B,), "q_len"),
             a.dense(kv_len, torch.int32, (p.B,), "kv_len"), a.strided(out, qs, "out"),
             a.dense(out2, a.dtype, qs, "out2"), a.dense(lse, torch.float32, _lse_shape(p), "lse")]
-    rc = load().sla_diff_forward(ctypes.byref(p), a.array(), *args, _ptr(ws), _nbytes(ws), _stream(stream))
+    rc = load().sla_diff_forward(ctypes.byref(p), a.array(), *args, *a.workspace(ws), a.stream(stream))
     _raise(rc, "sla_diff_forward")
     return out
 
@@ -495,7 +506,7 @@ def sla_diff_backward(p, q, k, v, lam, out, out2, lse, dout, dq, dk, dv, dlam, w
         ctypes.byref(p), a.array(), tq, tk, tv, a.dense(lam, a.dtype, (p.H,), "lam"),
         a.dense(q_len, torch.int32, (p.B,), "q_len"), a.dense(kv_len, torch.int32, (p.B,), "kv_len"), to,
         a.dense(out2, a.dtype, qs, "out2"), a.dense(lse, torch.float32, _lse_shape(p), "lse"), tdo, tdq, tdk, tdv,
-        a.dense(dlam, a.dtype, (p.H,), "dlam"), _ptr(ws), _nbytes(ws), _stream(stream))
+        a.dense(dlam, a.dtype, (p.H,), "dlam"), *a.workspace(ws), a.stream(stream))
     _raise(rc, "sla_diff_backward")
     return dq, dk, dv, dlam
 
@@ -512,6 +523,6 @@ def sla_prefix_forward(p, q, k_prefix, v_prefix, k, v, out, ws, lam=None, lse=No
             a.strided(k, ks, "k"), a.strided(v, ks, "v"), a.dense(lam, a.dtype, (p.H,), "lam"),
             a.dense(q_len, torch.int32, (p.B,), "q_len"), a.dense(kv_len, torch.int32, (p.B,), "kv_len"),
             a.strided(out, qs, "out"), a.dense(lse, torch.float32, _lse_shape(p), "lse")]
-    rc = load().sla_prefix_forward(ctypes.byref(p), a.array(), *args, _ptr(ws), _nbytes(ws), _stream(stream))
+    rc = load().sla_prefix_forward(ctypes.byref(p), a.array(), *args, *a.workspace(ws), a.stream(stream))
     _raise(rc, "sla_prefix_forward")
     return out
