@@ -156,6 +156,10 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, u
         "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(n), "r"(h), "r"(b)
         : "memory");
 }
+// Programmatic dependent launch: a kernel lets the next one of its stream start early, and that one waits here for
+// all of the first's work before it touches any of it.
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void reg_inc() {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -215,6 +219,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
 
     const int tid = threadIdx.x, warp = __shfl_sync(~0u, tid >> 5, 0), lane = tid & 31;
 
+    let_next_start();
     // ------------------------------------------------------------ which rows, which keys
     const bool gathered = static_cast<int>(blockIdx.x) < f.gathered_items;
     int it = gathered ? blockIdx.x : blockIdx.x - f.gathered_items;
@@ -318,29 +323,28 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
         for (int y = 0; y < SLOTS; ++y)     // every load has landed before the CTA exits
             if ((used >> y) & 1u) mbar_wait(&full[y], (last >> y) & 1u, abort_flag, drain_lim);
     } else if (warp == 1 || warp == 2) {
-        // ==================================================== MMA issuers, one a stream (the whole warp waits, one
-        // lane issues).  An issue blocks until the tensor core takes it, and a wait after it starts only then: with
-        // one issuer for both streams its waits left the tensor core idle for half of the time.
-        const int s = warp - 1;
+        // ==================================================== MMA issuers (the whole warp waits, one lane issues)
+        // One a stream: an issue blocks until the tensor core takes it, and a wait after it starts only then, so one
+        // issuer for both streams leaves the tensor core idle between them.  Every issuer waits for every load in
+        // order, so that it sees each phase of a slot; where the streams take different tiles that is one issuer for
+        // both (two of them, each with its own tiles alone, would mistake a slot's phases for each other).
         constexpr uint32_t ID_S = idesc_t<T>(128, kDenseBN, 0, 0), ID_O = idesc_t<T>(128, D, 0, 1);
         const bool leader = elect_one();
         auto wait = [&](uint64_t* bar, uint32_t par) { return warp_wait(bar, par, abort_flag, lim); };
-        const uint64_t q0 = sdesc(sbase + (two ? s * L::QTILE : 0), 16, 1024, kSwizzle128B),
-                       k0 = sdesc(sbase + L::OFF_RING, 16, 1024, kSwizzle128B),
+        const uint64_t q0 = sdesc(sbase, 16, 1024, kSwizzle128B), k0 = sdesc(sbase + L::OFF_RING, 16, 1024, kSwizzle128B),
                        v0 = sdesc(sbase + L::OFF_RING, L::BOX, 1024, kSwizzle128B);
-        const uint32_t S = tmem + s * 128, O = tmem + COL_O + s * D;
-        const int step = every ? 1 : 2, k_to_v = every ? 1 : 3;
-        RingPos<SLOTS> rp{every ? 0 : s, 0u};
-        // S of the stream's next tile
-        auto qk = [&]() {
+        const uint32_t q_step = two ? L::QTILE >> 4 : 0;
+        RingPos<SLOTS> rp{0, 0u};
+        // S of stream s from the key tile at rp
+        auto qk = [&](int s) {
             if (!wait(&full[rp.slot], rp.phase)) return false;
             if (leader) {
-                const uint64_t kd = k0 + rp.slot * (L::TILE >> 4);
+                const uint64_t qd = q0 + s * q_step, kd = k0 + rp.slot * (L::TILE >> 4);
                 constexpr int STEPS = DIFF ? D / 32 : D / 16;
 #pragma unroll
                 for (int k = 0; k < STEPS; ++k) {
                     const int kk = k + (DIFF ? s * STEPS : 0);
-                    umma_f16_ss(S, q0 + (((kk >> 2) * L::QBOX + (kk & 3) * 32) >> 4),
+                    umma_f16_ss(tmem + s * 128, qd + (((kk >> 2) * L::QBOX + (kk & 3) * 32) >> 4),
                                 kd + (((kk >> 2) * L::BOX + (kk & 3) * 32) >> 4), ID_S, k > 0 ? 1u : 0u);
                 }
                 umma_commit(&s_full[s]);
@@ -349,32 +353,46 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
             __syncwarp();
             return true;
         };
-        bool ok = n == 0 || wait(q_full, 0);
-        tc_fence_after();
-        int i = every ? 0 : s;
-        if (ok && i < n) ok = qk();
-        rp.step(every ? 1 : 2 + s);
-        for (uint32_t u = 0; ok && i < n; ++u) {
-            // P V of tile i, each half once its weights are there, then S of the stream's next tile
-            if (!(ok = wait(&full[rp.slot], rp.phase))) break;
+        // O_s += P_s V with the value tile i at rp, the stream's u-th, each half once its weights are there
+        auto pv = [&](int s, int i, uint32_t u) {
+            if (!wait(&full[rp.slot], rp.phase)) return false;
             if (i == dirty && leader) mbar_arrive(&v_here[s]);
             const uint64_t vd = v0 + rp.slot * (L::TILE >> 4);
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-                if (!(ok = wait(&p_full[2 * s + half], u & 1))) break;
+                if (!wait(&p_full[2 * s + half], u & 1)) return false;
                 tc_fence_after();
                 if (leader)
 #pragma unroll
                     for (int k = half * 4; k < half * 4 + 4; ++k)
-                        umma_f16_ts(O, S + k * 8, vd + ((k * 2048) >> 4), ID_O, (u > 0 || k > 0) ? 1u : 0u);
+                        umma_f16_ts(tmem + COL_O + s * D, tmem + s * 128 + k * 8, vd + ((k * 2048) >> 4), ID_O,
+                                    (u > 0 || k > 0) ? 1u : 0u);
             }
-            if (!ok) break;
             if (leader) umma_commit(&empty[rp.slot]);
             __syncwarp();
+            return true;
+        };
+        bool ok = n == 0 || wait(q_full, 0);
+        tc_fence_after();
+        if (every) {
+            const int s = warp - 1;
+            if (ok && n > 0) ok = qk(s);
             rp.step(1);
-            if (i + step < n) ok = qk();
-            rp.step(k_to_v);
-            i += step;
+            for (int i = 0; ok && i < n; ++i) {
+                if (!(ok = pv(s, i, i))) break;
+                rp.step(1);
+                if (i + 1 < n) ok = qk(s);
+                rp.step(1);
+            }
+        } else if (warp == 1) {
+            for (int i = 0; ok && i < min(n, 2); ++i, rp.step(1)) ok = qk(i);
+            if (n < 2) rp.step(2 - n);
+            for (int i = 0; ok && i < n; ++i) {
+                if (!(ok = pv(i & 1, i, i >> 1))) break;
+                rp.step(1);
+                if (i + 2 < n) ok = qk(i & 1);
+                rp.step(1);
+            }
         }
         if (!ok) fail();
         if (leader) umma_commit(o_full);   // also: every MMA has completed before tensor memory is released
@@ -629,19 +647,32 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
     if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
+__device__ __forceinline__ void unpack8(const uint4& w, float (&x)[8], __nv_bfloat16) {
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[2 * i] = bf16lo(u[i]), x[2 * i + 1] = bf16hi(u[i]);
+}
+__device__ __forceinline__ void unpack8(const uint4& w, float (&x)[8], __half) {
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[2 * i] = half_lo(u[i]), x[2 * i + 1] = half_hi(u[i]);
+}
+
 // Joins the parts of each row, a warp a row: weights 2^(lse_p - max), their sum,
-// the weighed mean of the parts' outputs.  Reads each part once.
+// the weighed mean of the parts' outputs.  A lane takes the log-sum-exps of every
+// 32nd part, and the outputs of eight parts are in flight at once (one part after
+// the other, 16 parts of 288 rows took 18 us).
 template <int D, typename T, bool DIFF>
-__global__ void __launch_bounds__(256) dense_merge_kernel(const __grid_constant__ DenseFwdArgs f) {
+__global__ void __launch_bounds__(128) dense_merge_kernel(const __grid_constant__ DenseFwdArgs f) {
     constexpr int C = D / 32, M = DIFF ? 2 : 1;
     const DenseArgs& a = f.a;
     const int lane = threadIdx.x & 31;
-    const long long row = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    const int row = static_cast<int>(blockIdx.x) * 4 + (threadIdx.x >> 5);
     if (row >= f.rows) return;
-    const int per_seq = a.G * a.Nq, lr = static_cast<int>(row % per_seq);
-    const int hk = static_cast<int>(row / per_seq % a.Hk), b = static_cast<int>(row / per_seq / a.Hk);
+    const int per_seq = a.G * a.Nq, lr = row % per_seq, hk = row / per_seq % a.Hk, b = row / per_seq / a.Hk;
     const int qi = lr / a.G, h = hk * a.G + lr % a.G;
     const int slots = f.slots_g + f.slots_b;
+    wait_for_previous();
     float o[M][C];
 #pragma unroll
     for (int x = 0; x < M; ++x) {
@@ -652,15 +683,34 @@ __global__ void __launch_bounds__(256) dense_merge_kernel(const __grid_constant_
 #pragma unroll
         for (int c = 0; c < C; ++c) o[x][c] = 0.f;
         if (mx > -INFINITY) {
-            for (int p = 0; p < slots; ++p) {
-                const long long at = (static_cast<long long>(p) * M + x) * f.rows + row;
-                const float w = fast_exp2(f.lpart[at] - mx);
-                if (!(w > 0.f)) continue;                      // nothing seen there: its output was not written
-                sum += w;
-                const float* src = f.opart + at * D + lane * C;
+            for (int p0 = 0; p0 < slots; p0 += 32) {
+                float mine = 0.f;                              // this lane's part's weight, 0 past the last
+                if (p0 + lane < slots)
+                    mine = fast_exp2(f.lpart[(static_cast<long long>(p0 + lane) * M + x) * f.rows + row] - mx);
+                sum += mine;
+                for (int y0 = 0; y0 < min(32, slots - p0); y0 += 8) {
+                    float w[8];
+                    float2 v[8][C / 2];
 #pragma unroll
-                for (int c = 0; c < C; ++c) o[x][c] = fmaf(w, src[c], o[x][c]);
+                    for (int y = 0; y < 8; ++y) {
+                        w[y] = __shfl_sync(~0u, mine, y0 + y);
+                        const float2* src = reinterpret_cast<const float2*>(
+                            f.opart + ((static_cast<long long>(p0 + y0 + y) * M + x) * f.rows + row) * D + lane * C);
+#pragma unroll
+                        for (int c = 0; c < C / 2; ++c)        // (a part that saw nothing was not written)
+                            v[y][c] = w[y] > 0.f ? src[c] : make_float2(0.f, 0.f);
+                    }
+#pragma unroll
+                    for (int y = 0; y < 8; ++y)
+#pragma unroll
+                        for (int c = 0; c < C / 2; ++c) {
+                            o[x][2 * c] = fmaf(w[y], v[y][c].x, o[x][2 * c]);
+                            o[x][2 * c + 1] = fmaf(w[y], v[y][c].y, o[x][2 * c + 1]);
+                        }
+                }
             }
+#pragma unroll
+            for (int y = 16; y; y >>= 1) sum += __shfl_xor_sync(~0u, sum, y);
             const float inv = 1.f / sum;
 #pragma unroll
             for (int c = 0; c < C; ++c) o[x][c] *= inv;
@@ -713,17 +763,6 @@ struct DenseBwdMaps {
     CUtensorMap q, dout, k, v;                      // box 64 x 64 tokens
 };
 
-__device__ __forceinline__ void unpack8(const uint4& w, float (&x)[8], __nv_bfloat16) {
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) x[2 * i] = bf16lo(u[i]), x[2 * i + 1] = bf16hi(u[i]);
-}
-__device__ __forceinline__ void unpack8(const uint4& w, float (&x)[8], __half) {
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) x[2 * i] = half_lo(u[i]), x[2 * i + 1] = half_hi(u[i]);
-}
-
 // The per-query values above, from one read of dout, out and out2:
 //   delta_2 = dout . out2,  delta_1 = dout . O_1 = dout . out + lambda delta_2.
 // One CTA a tile of 64 queries of a head, 8 lanes a row.
@@ -734,6 +773,7 @@ __global__ void __launch_bounds__(256) dense_rows_kernel(const __grid_constant__
     const int qn = dense_len(a.q_len, b, a.Nq), lane8 = threadIdx.x & 7;
     const float lam = to_f<T>(static_cast<const T*>(a.lam)[h]);
     if (b == 0 && t == 0 && threadIdx.x == 0) f.dlam_done[h] = 0u;
+    let_next_start();
 #pragma unroll
     for (int y = 0; y < 2; ++y) {
         const int c = y * 32 + (threadIdx.x >> 3), i = t * kDenseRowTile + c;
@@ -892,6 +932,7 @@ __device__ __forceinline__ void dense_bwd_cta(const DenseBwdMaps& tm, const Dens
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    wait_for_previous();                  // the row values
     const uint32_t tmem = *tmem_slot;
     const unsigned long long lim = f.wait_ns, drain_lim = 4000000000ull;
     auto fail = [&]() {

@@ -64,29 +64,29 @@ DensePlan dense_plan(const sla_dense_params_t* p) {
     x.rows = all * p->Hk;
     // The prefix is taken for all sequences at once where a sequence alone leaves most of a row tile empty.
     const bool gather = p->P > 0 && p->B > 1 && seq < 128;
+    x.prefix_b = !gather;
     auto shape = [&](long long rows, int& tiles, int& two) {
         two = !diff && rows > 128;
         tiles = static_cast<int>(cdiv(rows, two ? 256 : 128));
     };
     shape(seq, x.tiles_b, x.two_b);
-    x.prefix_b = !gather;
-    const long long tb = nK + (gather ? 0 : nP), cb = static_cast<long long>(p->B) * p->Hk * x.tiles_b;
-    long long work = cb * tb, cg = 0;
-    if (gather) {
-        shape(all, x.tiles_g, x.two_g);
-        cg = static_cast<long long>(p->Hk) * x.tiles_g;
-        work += cg * nP;
-    }
-    // A range of key tiles a CTA: where there are few CTAs, three ranges for each SM's share, so that sequences of
-    // different lengths even out, but eight tiles (two where that would leave SMs without a CTA): a CTA's start and the
-    // join cost as much as about that many.
-    const long long share = std::max<long long>(work >= 8 * SMS ? 8 : 2, cdiv(work, 3 * SMS));
-    x.splits_b = static_cast<int>(cb >= 3 * SMS ? 1 : std::max<long long>(1, std::min(cdiv(tb, share), 3 * SMS / cb)));
-    x.splits_g = gather ? static_cast<int>(std::max<long long>(1, cdiv(nP, share))) : 0;
+    if (gather) shape(all, x.tiles_g, x.two_g);
+    const long long tb = nK + (gather ? 0 : nP);                       // key tiles of a unit
+    const long long cb = gather && nK == 0 ? 0 : static_cast<long long>(p->B) * p->Hk * x.tiles_b,
+                    cg = gather ? static_cast<long long>(p->Hk) * x.tiles_g : 0;
+    const long long work = cb * tb + cg * nP;
+    // Ranges of key tiles that give each SM one CTA, of eight tiles at least where there is that much work, else two
+    // (a CTA's start, about 2.5 us, its end and the join cost as much as about that many).  More ranges, to even out
+    // sequences of different lengths, cost what they gave: 32 such caches, 1 range each 118 us, 2 and 4: 116, 6: 121.
+    const long long least = std::max<long long>(work >= 8 * SMS ? 8 : 2, cdiv(work, SMS));
+    auto ranges = [&](long long units, long long tiles) {
+        return units == 0 ? 0 : units >= SMS ? 1 : static_cast<int>(std::max<long long>(1, std::min(cdiv(tiles, least), SMS / units)));
+    };
+    x.splits_b = ranges(cb, tb);
+    x.splits_g = ranges(cg, nP);
     // a stream of every second tile is a part of its own
     x.slots_b = x.splits_b * (!diff && !x.two_b ? 2 : 1);
-    x.slots_g = gather ? x.splits_g * (!diff && !x.two_g ? 2 : 1) : 0;
-    if (gather && p->Nk == 0) x.slots_b = x.splits_b = 0;
+    x.slots_g = x.splits_g * (!diff && !x.two_g ? 2 : 1);
     x.gathered_items = static_cast<int>(cg * x.splits_g);
     x.items = x.gathered_items + static_cast<int>(cb * x.splits_b);
     x.direct = x.slots_b + x.slots_g == 1;
@@ -121,11 +121,24 @@ DenseWs dense_layout(const sla_dense_params_t* p) {
     return w;
 }
 
+// A launch; `early`: it may start before the kernel ahead of it in the stream has ended (and waits inside for that).
+template <typename... P, typename... A>
+cudaError_t dense_go(void (*kern)(P...), unsigned grid, unsigned threads, int smem, cudaStream_t st, bool early,
+                     const A&... args) {
+    cudaLaunchConfig_t c{};
+    c.gridDim = dim3(grid), c.blockDim = dim3(threads), c.dynamicSmemBytes = static_cast<size_t>(smem), c.stream = st;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    c.attrs = &at, c.numAttrs = early ? 1 : 0;
+    return cudaLaunchKernelEx(&c, kern, args...);
+}
+
 // Shared memory above the default is asked for once a kernel and device, and again if a launch says it is not there
 // (a context that was reset).
-template <typename K, typename... A>
-sla_status_t dense_launch(K* kern, std::atomic<unsigned long long>& asked, unsigned grid, int smem, cudaStream_t st,
-                          const A&... args) {
+template <typename... P, typename... A>
+sla_status_t dense_launch(void (*kern)(P...), std::atomic<unsigned long long>& asked, unsigned grid, int smem,
+                          cudaStream_t st, bool early, const A&... args) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return SLA_ERR_CUDA;
     const unsigned long long bit = 1ull << (dev & 63);
@@ -136,8 +149,8 @@ sla_status_t dense_launch(K* kern, std::atomic<unsigned long long>& asked, unsig
                 return SLA_ERR_CUDA;
             asked.fetch_or(bit, std::memory_order_relaxed);
         }
-        kern<<<grid, sla::kDenseThreads, smem, st>>>(args...);
-        if (cudaGetLastError() == cudaSuccess) return SLA_OK;
+        if (dense_go(kern, grid, sla::kDenseThreads, smem, st, early, args...) == cudaSuccess) return SLA_OK;
+        cudaGetLastError();
         if (fresh) break;
     }
     return SLA_ERR_CUDA;
@@ -211,12 +224,14 @@ sla_status_t dense_fwd_t(const sla_dense_params_t* p, const sla::DenseArgs& a, v
     {
         Span sp(SLA_KERNEL_DENSE, st);
         const sla_status_t s = dense_launch(sla::dense_fwd_kernel<D, T, DIFF>, asked, static_cast<unsigned>(x.items),
-                                            L::SMEM, st, tm, f);
+                                            L::SMEM, st, false, tm, f);
         if (s != SLA_OK) return s;
     }
     if (!x.direct) {
         Span sp(SLA_KERNEL_DENSE, st);
-        sla::dense_merge_kernel<D, T, DIFF><<<static_cast<unsigned>((x.rows + 7) / 8), 256, 0, st>>>(f);
+        if (dense_go(sla::dense_merge_kernel<D, T, DIFF>, static_cast<unsigned>((x.rows + 3) / 4), 128, 0, st, true, f) !=
+            cudaSuccess)
+            return SLA_ERR_CUDA;
     }
     return launch_status();
 }
@@ -257,7 +272,7 @@ sla_status_t dense_bwd(const sla_dense_params_t* p, const sla::DenseArgs& a, voi
         Span sp(SLA_KERNEL_DENSE_BWD, st);
         const sla_status_t s = dense_launch(sla::dense_bwd_kernel<D, T>, asked,
                                             static_cast<unsigned>(f.key_items + p->B * p->H * f.query_tiles), L::SMEM, st,
-                                            tm, f);
+                                            true, tm, f);
         if (s != SLA_OK) return s;
     }
     return launch_status();

@@ -157,6 +157,12 @@ PREFIX = [  # B, H, Hk, Nq, Nk, P, d, dtype, causal, diff, q_len, kv_len
     (2, 2, 2, 200, 0, 200, 128, "bf16", True, True, [200, 5], None),
     (2, 2, 2, 4, 0, 0, 64, "bf16", False, False, None, None),               # nothing at all
     (70, 4, 1, 2, 130, 2000, 128, "bf16", True, False, None, None),
+    # long walks of a CTA over its keys, in each way the rows can be tiled
+    (40, 12, 4, 1, 8192, 0, 128, "bf16", True, False, None, None),
+    (50, 12, 4, 1, 6000, 0, 64, "fp16", True, False, None, [6000 - 97 * i for i in range(50)]),
+    (2, 160, 160, 1, 100, 5000, 64, "bf16", True, False, None, None),
+    (1, 80, 80, 129, 3000, 1000, 128, "bf16", True, False, None, None),
+    (40, 12, 4, 1, 5000, 0, 128, "bf16", True, True, None, None),
 ]
 
 
