@@ -103,6 +103,7 @@ struct DenseFwdArgs {
     int slots_g, slots_b;
     long long rows;                                // B * Hk * G * Nq
     unsigned long long wait_ns;
+    int debug_stall;                               // test hook: load no tiles, so the consumers' waits run out
 };
 
 template <int D, bool DIFF>
@@ -311,12 +312,13 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
             last = (last & ~(1u << rp.slot)) | ((rp.phase ^ 1u) << rp.slot);
             return true;
         };
+        const int n_load = f.debug_stall ? 0 : n;
         for (int i = 0; ok && i < lead; ++i, rp.step(1))
-            if (i < n) ok = load(i, false);
-        for (int i = 0; ok && i < n; ++i) {
+            if (i < n_load) ok = load(i, false);
+        for (int i = 0; ok && i < n_load; ++i) {
             ok = load(i, true);
             rp.step(1);
-            if (ok && i + lead < n) ok = load(i + lead, false);
+            if (ok && i + lead < n_load) ok = load(i + lead, false);
             rp.step(1);
         }
         if (!ok) fail();
@@ -739,14 +741,15 @@ __global__ void __launch_bounds__(128) dense_merge_kernel(const __grid_constant_
 // each query: kDenseRowFloats values for 64 queries, in the order
 //   -lse_1 log2 e + shift | -lse_2 log2 e + shift | -delta_1 2^-shift | -delta_2 2^-shift
 // (-inf, 0 for padding and queries that see nothing, whose weights so become 0).
-// shift is 10 for fp16: P 2^10 keeps the weights of rows of thousands of keys
-// out of the subnormal range (2^-14); W = P_1 - lambda P_2 enters its product
-// scaled and dv is scaled back, dS = (P 2^10) ((dP - delta) 2^-10) is not scaled.
+// shift is 6 for fp16: P 2^6 keeps the weights of rows of thousands of keys out of
+// the subnormal range (2^-14), and leaves lambda room up to 1000; W = P_1 - lambda
+// P_2 enters its product scaled and dv is scaled back, dS = (P 2^6) ((dP - delta)
+// 2^-6) is not scaled.
 constexpr int kDenseRowTile = 64, kDenseRowFloats = 4 * kDenseRowTile;
 template <typename T>
-constexpr float kDenseShift = std::is_same<T, __half>::value ? 10.f : 0.f;
+constexpr float kDenseShift = std::is_same<T, __half>::value ? 6.f : 0.f;
 template <typename T>
-constexpr float kDenseUnshift = std::is_same<T, __half>::value ? 9.765625e-4f : 1.f;
+constexpr float kDenseUnshift = std::is_same<T, __half>::value ? 0.015625f : 1.f;
 
 struct DenseBwdArgs {
     DenseArgs a;
@@ -757,6 +760,7 @@ struct DenseBwdArgs {
     float* dlam_part;                               // [H][B][query_tiles] sums of delta_2
     unsigned* dlam_done;                            // [H] how many of a head's are there
     unsigned long long wait_ns;
+    int debug_stall;                                // test hook, as above
 };
 
 struct DenseBwdMaps {
@@ -945,7 +949,8 @@ __device__ __forceinline__ void dense_bwd_cta(const DenseBwdMaps& tm, const Dens
         // ==================================================== producer (the whole warp waits, one lane issues)
         const bool leader = elect_one();
         const CUtensorMap *mx = KEYS ? &tm.q : &tm.k, *my = KEYS ? &tm.dout : &tm.v;
-        if (KEYS && n > 0 && leader) {
+        const int n_load = f.debug_stall ? 0 : n;
+        if (KEYS && n_load > 0 && leader) {
             mbar_arrive_expect_tx(r_full, 2 * L::RES);
             for (int c = 0; c < NBOX; ++c)
                 for (int z = 0; z < 2; ++z) {
@@ -960,7 +965,7 @@ __device__ __forceinline__ void dense_bwd_cta(const DenseBwdMaps& tm, const Dens
         RingPos<SLOTS> rp{0, 1u};           // (phase of the wait for an empty slot: the first round passes)
         bool ok = true;
         int i = 0, t = t0, h = KEYS ? hr * a.G : hk;
-        for (; i < n; ++i) {
+        for (; i < n_load; ++i) {
             if (!(ok = wait(&empty[rp.slot], rp.phase))) break;
             if (leader) {
                 unsigned char* st = smem + L::OFF_RING + rp.slot * L::STAGE;
@@ -982,7 +987,7 @@ __device__ __forceinline__ void dense_bwd_cta(const DenseBwdMaps& tm, const Dens
         }
         if (!ok) fail();
         // every load has landed before the CTA exits
-        if (KEYS && n > 0) mbar_wait(r_full, 0, abort_flag, drain_lim);
+        if (KEYS && n_load > 0) mbar_wait(r_full, 0, abort_flag, drain_lim);
         for (int y = max(0, i - SLOTS); y < i; ++y) mbar_wait(&full[y % SLOTS], (y / SLOTS) & 1, abort_flag, drain_lim);
     } else if (warp == 1) {
         // ==================================================== issuer of S and dP

@@ -212,6 +212,7 @@ sla_status_t dense_fwd_t(const sla_dense_params_t* p, const sla::DenseArgs& a, v
     f.slots_g = x.slots_g, f.slots_b = x.slots_b, f.rows = x.rows;
     f.opart = at<float>(ws, w.opart), f.lpart = at<float>(ws, w.lpart);
     f.wait_ns = wait_limit_ns();
+    f.debug_stall = debug_stall() ? 1 : 0;
     sla::DenseMaps tm{};
     constexpr bool half = std::is_same<T, __half>::value;
     if (p->Nk && (!dense_map(&tm.k, a.k, a.ks, p->B, p->Hk, p->Nk, D, half) ||
@@ -256,6 +257,7 @@ sla_status_t dense_bwd(const sla_dense_params_t* p, const sla::DenseArgs& a, voi
     f.key_items = p->B * p->Hk * f.key_tiles;
     f.rowdata = at<float>(ws, w.rowdata), f.dlam_part = at<float>(ws, w.dlam_part), f.dlam_done = at<unsigned>(ws, w.dlam_done);
     f.wait_ns = wait_limit_ns();
+    f.debug_stall = debug_stall() ? 1 : 0;
     sla::DenseBwdMaps tm{};
     constexpr bool half = std::is_same<T, __half>::value;
     if (!dense_map(&tm.q, a.q, a.qs, p->B, p->H, p->Nq, D, half, 64) ||
@@ -335,6 +337,8 @@ extern "C" sla_status_t sla_diff_backward(const sla_dense_params_t* p, const int
     if (p->Nk && ((s = check_tensor(k, 16)) || (s = check_tensor(v, 16)) || (s = check_tensor(dk, 16)) ||
                   (s = check_tensor(dv, 16))))
         return s;
+    // (broadcast keys of a size that no gradient has room for)
+    if (static_cast<long long>(p->B) * p->Hk * ((p->Nk + 127) / 128) > (1LL << 30)) return SLA_ERR_UNSUPPORTED;
     sla::DenseArgs a{};
     struct { sla::DenseT* t; int h, n; bool output; } const want[8] = {
         {&a.qs, p->H, p->Nq, false}, {&a.ks, p->Hk, p->Nk, false}, {&a.vs, p->Hk, p->Nk, false},

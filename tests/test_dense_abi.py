@@ -66,6 +66,12 @@ def test_parameters(lib, kw, code):
         S.dense_workspace(p)
 
 
+def test_gradients_of_more_keys_than_memory_has_room_for(lib):
+    p = pd(B=4096, H=64, Hk=64, Nq=1, Nk=1 << 20)
+    st = i64(*[64] * 24)
+    assert bwd(lib, p, st=st) == UNSUPPORTED
+
+
 def test_null_parameters_and_flags(lib):
     assert lib.sla_dense_workspace_size(None) == 0
     assert lib.sla_diff_forward(None, None, *[FAKE] * 10, BIG, None) == INVALID

@@ -129,6 +129,8 @@ BWD = [
     (2, 6, 2, 70, 300, 128, "fp16", True, [70, 3], [40, 299]),
     (1, 2, 2, 700, 900, 128, "bf16", True, None, None),
     (1, 8, 1, 1, 1000, 64, "bf16", True, None, None),
+    (1, 2, 1, 2500, 2500, 64, "fp16", True, None, None),      # long walks; weights near fp16's smallest
+    (1, 2, 2, 3, 6000, 128, "fp16", False, None, None),
 ]
 
 
@@ -351,4 +353,27 @@ def test_gradients_against_differences():
         third = (exact[0] - exact[1] - ((ends[0][1] - ends[1][1]) * R.dense(**x, causal=True)[n]).sum()).abs()
         bound = 2.2 * (x["dout"].double().abs() * tol).sum() + third
         assert (f[0] - f[1] - want).abs() <= bound + 2.0 ** -10 * want.abs(), (n, f, want, bound)
+    ok()
+
+
+@pytest.mark.parametrize("Nq", [300, 1])
+def test_waits_that_run_out_are_reported_and_the_context_survives(Nq, monkeypatch):
+    """With the test hook the loaders issue no loads, so the consumers' bounded waits (2 ms here) run out: a
+    status, no fault, and the next call is right."""
+    x = make(2, 4, 2, Nq, 300, 128, grads=True)
+    y = make(3, 4, 2, Nq, 200, 64, P=500, diff=False)
+    r = backward(x, forward(x, True))
+    ok()
+    monkeypatch.setenv("SLA_DEBUG_STALL", "1")
+    monkeypatch.setenv("SLA_DEBUG_WAIT_LIMIT_NS", "2000000")
+    forward(x, True)
+    assert S.sla_check_device_status() == S.sla.SLA_ERR_TIMEOUT
+    backward(x, dict(r))
+    assert S.sla_check_device_status() == S.sla.SLA_ERR_TIMEOUT
+    prefix(y, 500, True)
+    assert S.sla_check_device_status() == S.sla.SLA_ERR_TIMEOUT
+    monkeypatch.undo()
+    r = backward(x, forward(x, True))
+    R.check(r, R.dense(**x, causal=True), ("out", "dq", "dk", "dv", "dlam"))
+    R.check(prefix(y, 500, True), R.dense(**y, causal=True), ("out", "lse"))
     ok()
