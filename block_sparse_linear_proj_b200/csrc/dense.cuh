@@ -44,14 +44,15 @@ template <>
 __device__ __forceinline__ __half from_f<__half>(float x) { return __float2half_rn(x); }
 
 // A sequence's length: within [0, most], out-of-range values flagged.
-__device__ __forceinline__ int dense_len(const int32_t* len, int b, int most) {
-    if (!len) return most;
-    const int n = len[b];
+__device__ __forceinline__ int dense_len_in(int n, int most) {
     if (n < 0 || n > most) {
         report(kStatusBadData);
         return n < 0 ? 0 : most;
     }
     return n;
+}
+__device__ __forceinline__ int dense_len(const int32_t* len, int b, int most) {
+    return len ? dense_len_in(len[b], most) : most;
 }
 
 // ------------------------------------------------------------------ forward
@@ -239,7 +240,9 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
     const int per_seq = a.G * a.Nq;
     const int rows = gathered ? a.B * per_seq : per_seq;
     const int row0 = tile * (two ? 256 : 128);
-    const int qn0 = gathered ? 0 : dense_len(a.q_len, b0, a.Nq), kn0 = gathered ? 0 : dense_len(a.kv_len, b0, a.Nk);
+    // (both lengths are asked for before either is looked at)
+    const int q_raw = !gathered && a.q_len ? a.q_len[b0] : a.Nq, k_raw = !gathered && a.kv_len ? a.kv_len[b0] : a.Nk;
+    const int qn0 = gathered ? 0 : dense_len_in(q_raw, a.Nq), kn0 = gathered ? 0 : dense_len_in(k_raw, a.Nk);
     const int nP = (gathered || f.prefix_b) ? (a.P + kDenseBN - 1) / kDenseBN : 0;
     int own = 0;                                   // own keys that the last query of these rows sees
     if (!gathered) {
@@ -423,23 +426,28 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
         };
         const int my_row = (two ? s * 128 : 0) + r;
         if (n > 0) {
-            // the query rows, a thread a row (or half of one): zeros where there is no query.  All of a thread's loads
-            // are in flight at once (one chunk of a row after the other took up to 11 us for 256 gathered rows)
-            constexpr int CH = D / 16;                          // 16-byte chunks of half a row
-            const int rr = two ? tid - 128 : (tid - 128) & 127;
-            const Row x = row_of(rr);
-            const uint4* src = reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) +
-                                                              (x.real ? a.qs.at(x.b, x.h, x.qi) : 0));
+            // the query rows, zeros where there is no query: a lane finds the place of one row, D/8 lanes load a row, and
+            // four of a lane's loads are in flight at once (a 16-byte chunk of a row of its own for each lane took up to
+            // 6 us for 256 gathered rows)
+            constexpr int LANES = D / 8;                        // 16-byte chunks a row
+            const int per_warp = two ? 32 : 16, first = (warp - 4) * per_warp;
+            const Row x = row_of(first + lane % per_warp);
+            const T* mine = x.real ? static_cast<const T*>(a.q) + a.qs.at(x.b, x.h, x.qi) : nullptr;
+            const int c = lane % LANES;
+#pragma unroll 1
+            for (int y0 = 0; y0 < per_warp; y0 += 4 * (32 / LANES)) {
+                uint4 v[4];
 #pragma unroll
-            for (int z = 0; z < 2; ++z) {
-                if (!two && z != s) continue;
-                uint4 v[CH];
+                for (int z = 0; z < 4; ++z) {
+                    const char* src = reinterpret_cast<const char*>(__shfl_sync(
+                        ~0u, reinterpret_cast<unsigned long long>(mine), y0 + z * (32 / LANES) + lane / LANES));
+                    v[z] = src ? __ldg(reinterpret_cast<const uint4*>(src) + c) : make_uint4(0, 0, 0, 0);
+                }
 #pragma unroll
-                for (int c = 0; c < CH; ++c) v[c] = x.real ? __ldg(src + z * CH + c) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-                for (int c = 0; c < CH; ++c)
-                    *reinterpret_cast<uint4*>(smem + (rr >> 7) * L::QTILE + ((z * CH + c) >> 3) * L::QBOX +
-                                              sw128(rr & 127, (z * CH + c) & 7)) = v[c];
+                for (int z = 0; z < 4; ++z) {
+                    const int rr = first + y0 + z * (32 / LANES) + lane / LANES;
+                    *reinterpret_cast<uint4*>(smem + (rr >> 7) * L::QTILE + (c >> 3) * L::QBOX + sw128(rr & 127, c & 7)) = v[z];
+                }
             }
             fence_proxy_async_smem();
             __syncwarp();
@@ -566,11 +574,13 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
             *reinterpret_cast<uint4*>(stage + at + lane * row_bytes + ((chunk ^ (lane & 3)) << 4)) = v;
         };
         auto flush = [&](int at, auto row_bytes, void* dst) {
-            constexpr int RB = decltype(row_bytes)::value, LANES = RB / 16;
+            constexpr int RB = decltype(row_bytes)::value, LANES = RB / 16, AT_ONCE = 32 / LANES;
+            const unsigned wanted = __ballot_sync(~0u, dst != nullptr);
             const int c = lane % LANES;
 #pragma unroll 4
             for (int y = 0; y < LANES; ++y) {
-                const int rr = y * (32 / LANES) + lane / LANES;
+                if (!((wanted >> (y * AT_ONCE)) & ((1u << AT_ONCE) - 1u))) continue;
+                const int rr = y * AT_ONCE + lane / LANES;
                 char* to = reinterpret_cast<char*>(__shfl_sync(~0u, reinterpret_cast<unsigned long long>(dst), rr));
                 const uint4 v = *reinterpret_cast<const uint4*>(stage + at + rr * RB + ((c ^ (rr & 3)) << 4));
                 if (to) reinterpret_cast<uint4*>(to)[c] = v;
@@ -613,9 +623,9 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
                 flush(32 * D, std::integral_constant<int, D>{},
                       write ? static_cast<T*>(a.out2) + ((static_cast<long long>(b) * a.H + h) * a.Nq + qi) * D + s * (D / 2)
                             : nullptr);
-        } else {
+        } else if (__any_sync(~0u, in && ok && (f.direct || l > 0.f))) {
             const float inv = l > 0.f ? 1.f / l : 0.f;
-#pragma unroll 1
+#pragma unroll 2
             for (int x = 0; x < D; x += 16) {
                 uint32_t o[16];
                 tmem_ld16(tl + COL_O + s * D + x, o);
@@ -899,7 +909,8 @@ __device__ __forceinline__ void dense_bwd_cta(const DenseBwdMaps& tm, const Dens
     const int hr = item / tiles % heads, b = item / tiles / heads;
     const int hk = KEYS ? hr : hr / a.G;
     const int row0 = tile * 128;
-    const int qn = dense_len(a.q_len, b, a.Nq), kn = dense_len(a.kv_len, b, a.Nk), off = kn - qn;
+    const int q_raw = a.q_len ? a.q_len[b] : a.Nq, k_raw = a.kv_len ? a.kv_len[b] : a.Nk;
+    const int qn = dense_len_in(q_raw, a.Nq), kn = dense_len_in(k_raw, a.Nk), off = kn - qn;
     int t0 = 0, per = 0;                  // streamed tiles [t0, t0 + per) of each head
     if (KEYS) {
         if (row0 < kn) {
