@@ -222,6 +222,10 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
     const int tid = threadIdx.x, warp = __shfl_sync(~0u, tid >> 5, 0), lane = tid & 31;
 
     let_next_start();
+    if (warp == 1) {
+        tmem_alloc(tmem_slot, 512);
+        tmem_relinquish();
+    }
     // ------------------------------------------------------------ which rows, which keys
     const bool gathered = static_cast<int>(blockIdx.x) < f.gathered_items;
     int it = gathered ? blockIdx.x : blockIdx.x - f.gathered_items;
@@ -271,10 +275,6 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
         mbar_init(o_full, 2);
         *abort_flag = 0;
         fence_barrier_init();
-    }
-    if (warp == 1) {
-        tmem_alloc(tmem_slot, 512);
-        tmem_relinquish();
     }
     tc_fence_before();
     __syncthreads();
@@ -596,13 +596,13 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
             const float lam = to_f<T>(static_cast<const T*>(a.lam)[h]);
             const bool second = a.out2 != nullptr;
 #pragma unroll 1
-            for (int x = 0; x < D / 2; x += 16) {
-                uint32_t o1[16], o2[16], w1[8], w2[8];
-                tmem_ld16(tl + COL_O + s * (D / 2) + x, o1);
-                tmem_ld16(tl + COL_O + D + s * (D / 2) + x, o2);
+            for (int x = 0; x < D / 2; x += 32) {
+                uint32_t o1[32], o2[32], w1[16], w2[16];
+                tmem_ld32(tl + COL_O + s * (D / 2) + x, o1);
+                tmem_ld32(tl + COL_O + D + s * (D / 2) + x, o2);
                 tmem_ld_wait();
 #pragma unroll
-                for (int y = 0; y < 8; ++y) {
+                for (int y = 0; y < 16; ++y) {
                     const float a0 = l2 > 0.f ? __uint_as_float(o2[2 * y]) * i2 : 0.f,
                                 a1 = l2 > 0.f ? __uint_as_float(o2[2 * y + 1]) * i2 : 0.f,
                                 b0_ = l1 > 0.f ? __uint_as_float(o1[2 * y]) * i1 : 0.f,
@@ -611,7 +611,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
                     w2[y] = pack2<T>(a0, a1);
                 }
 #pragma unroll
-                for (int y = 0; y < 2; ++y) {
+                for (int y = 0; y < 4; ++y) {
                     put(0, D, x / 8 + y, make_uint4(w1[4 * y], w1[4 * y + 1], w1[4 * y + 2], w1[4 * y + 3]));
                     if (second) put(32 * D, D, x / 8 + y, make_uint4(w2[4 * y], w2[4 * y + 1], w2[4 * y + 2], w2[4 * y + 3]));
                 }
@@ -625,16 +625,17 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
                             : nullptr);
         } else if (__any_sync(~0u, in && ok && (f.direct || l > 0.f))) {
             const float inv = l > 0.f ? 1.f / l : 0.f;
-#pragma unroll 2
-            for (int x = 0; x < D; x += 16) {
-                uint32_t o[16];
-                tmem_ld16(tl + COL_O + s * D + x, o);
+#pragma unroll 1
+            for (int x = 0; x < D; x += 64) {
+                uint32_t o[64];
+                tmem_ld32(tl + COL_O + s * D + x, *reinterpret_cast<uint32_t(*)[32]>(o));
+                tmem_ld32(tl + COL_O + s * D + x + 32, *reinterpret_cast<uint32_t(*)[32]>(o + 32));
                 tmem_ld_wait();
 #pragma unroll
-                for (int y = 0; y < 16; ++y) o[y] = l > 0.f ? __float_as_uint(__uint_as_float(o[y]) * inv) : 0u;
+                for (int y = 0; y < 64; ++y) o[y] = l > 0.f ? __float_as_uint(__uint_as_float(o[y]) * inv) : 0u;
                 if (f.direct) {
 #pragma unroll
-                    for (int y = 0; y < 2; ++y) {
+                    for (int y = 0; y < 8; ++y) {
                         uint32_t w[4];
 #pragma unroll
                         for (int z = 0; z < 4; ++z)
@@ -643,7 +644,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
                     }
                 } else {
 #pragma unroll
-                    for (int y = 0; y < 4; ++y)
+                    for (int y = 0; y < 16; ++y)
                         put(0, 4 * D, x / 4 + y, make_uint4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]));
                 }
             }
