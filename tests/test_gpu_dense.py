@@ -159,6 +159,13 @@ PREFIX = [  # B, H, Hk, Nq, Nk, P, d, dtype, causal, diff, q_len, kv_len
     (2, 2, 2, 200, 0, 200, 128, "bf16", True, True, [200, 5], None),
     (2, 2, 2, 4, 0, 0, 64, "bf16", False, False, None, None),               # nothing at all
     (70, 4, 1, 2, 130, 2000, 128, "bf16", True, False, None, None),
+    # few rows against few keys
+    (3, 8, 1, 1, 1024, 0, 128, "bf16", True, True, None, [1024, 17, 0]),
+    (2, 4, 4, 8, 100, 0, 64, "fp16", True, False, [8, 3], [100, 2]),
+    (4, 4, 2, 1, 0, 1000, 128, "bf16", False, True, None, None),
+    (3, 6, 3, 1, 15, 900, 64, "bf16", True, True, None, [15, 1, 0]),
+    (64, 16, 2, 1, 700, 3000, 128, "fp16", True, True, None, [700 - 11 * i for i in range(64)]),
+    (9, 1, 1, 1, 33, 1024, 128, "bf16", True, False, None, None),
     # long walks of a CTA over its keys, in each way the rows can be tiled
     (40, 12, 4, 1, 8192, 0, 128, "bf16", True, False, None, None),
     (50, 12, 4, 1, 6000, 0, 64, "fp16", True, False, None, [6000 - 97 * i for i in range(50)]),
@@ -356,12 +363,12 @@ def test_gradients_against_differences():
     ok()
 
 
-@pytest.mark.parametrize("Nq", [300, 1])
-def test_waits_that_run_out_are_reported_and_the_context_survives(Nq, monkeypatch):
+@pytest.mark.parametrize("Nq,Nk,P", [(300, 300, 500), (1, 1300, 1500)])
+def test_waits_that_run_out_are_reported_and_the_context_survives(Nq, Nk, P, monkeypatch):
     """With the test hook the loaders issue no loads, so the consumers' bounded waits (2 ms here) run out: a
     status, no fault, and the next call is right."""
-    x = make(2, 4, 2, Nq, 300, 128, grads=True)
-    y = make(3, 4, 2, Nq, 200, 64, P=500, diff=False)
+    x = make(2, 4, 2, Nq, Nk, 128, grads=True)
+    y = make(3, 4, 2, Nq, 200, 64, P=P, diff=False)
     r = backward(x, forward(x, True))
     ok()
     monkeypatch.setenv("SLA_DEBUG_STALL", "1")
@@ -370,10 +377,10 @@ def test_waits_that_run_out_are_reported_and_the_context_survives(Nq, monkeypatc
     assert S.sla_check_device_status() == S.sla.SLA_ERR_TIMEOUT
     backward(x, dict(r))
     assert S.sla_check_device_status() == S.sla.SLA_ERR_TIMEOUT
-    prefix(y, 500, True)
+    prefix(y, P, True)
     assert S.sla_check_device_status() == S.sla.SLA_ERR_TIMEOUT
     monkeypatch.undo()
     r = backward(x, forward(x, True))
     R.check(r, R.dense(**x, causal=True), ("out", "dq", "dk", "dv", "dlam"))
-    R.check(prefix(y, 500, True), R.dense(**y, causal=True), ("out", "lse"))
+    R.check(prefix(y, P, True), R.dense(**y, causal=True), ("out", "lse"))
     ok()
