@@ -750,17 +750,32 @@ __global__ void __launch_bounds__(128) dense_merge_kernel(const __grid_constant_
 // ------------------------------------------------------------------ gradients
 // Rows the gradient kernel streams past its resident tile, and what it reads of
 // each query: kDenseRowFloats values for 64 queries, in the order
-//   -lse_1 log2 e + shift | -lse_2 log2 e + shift | -delta_1 2^-shift | -delta_2 2^-shift
+//   -lse_1 log2 e + shift | -lse_2 log2 e + shift | -delta_1 2^-shift | -delta_2 2^-shift | delta_1 - delta_2
 // (-inf, 0 for padding and queries that see nothing, whose weights so become 0).
 // shift is 6 for fp16: P 2^6 keeps the weights of rows of thousands of keys out of
 // the subnormal range (2^-14), and leaves lambda room up to 1000; W = P_1 - lambda
 // P_2 enters its product scaled and dv is scaled back, dS = (P 2^6) ((dP - delta)
 // 2^-6) is not scaled.
-constexpr int kDenseRowTile = 64, kDenseRowFloats = 4 * kDenseRowTile;
+constexpr int kDenseRowTile = 64, kDenseRowFloats = 5 * kDenseRowTile;
 template <typename T>
 constexpr float kDenseShift = std::is_same<T, __half>::value ? 6.f : 0.f;
 template <typename T>
 constexpr float kDenseUnshift = std::is_same<T, __half>::value ? 0.015625f : 1.f;
+
+// For the key side the same values of a tile also lie as an operand of the S and dP
+// products, 64 rows of 128 bytes in the 128-byte swizzle: elements 0-2, 16-18 and
+// 32-34 of a query's row are -lse_1, -lse_2 (as above, over tau log2 e) and -delta_1
+// in three parts of the I/O type each.  One further step of 16 against rows of the
+// parts' weights adds them, where reading them from shared memory for every lane
+// took 1024 of a tile's 2500 cycles.  bf16: weights 1, the parts hold 24 bits.
+// fp16: weights 2^14, 2^3, 2^-8; values to 2^29 (a part's remainder is at most 2^-11
+// of it: 2^18 fits 2^3 x 65504, 2^7 fits 2^-8 x 65504), to 2^-33 of 1 or of the value.
+constexpr int kDenseExt = 64 * 128;
+template <typename T>
+__device__ __forceinline__ float dense_ext_weight(int part) {
+    if (!std::is_same<T, __half>::value) return 1.f;
+    return part == 0 ? 16384.f : part == 1 ? 8.f : 1.f / 256.f;
+}
 
 struct DenseBwdArgs {
     DenseArgs a;
@@ -768,6 +783,7 @@ struct DenseBwdArgs {
     int key_items, key_tiles, query_tiles;          // CTAs of 128 keys, then CTAs of 128 queries
     int row_tiles;                                  // ceil(Nq / 64)
     float* rowdata;                                 // [B * H][row_tiles][kDenseRowFloats]
+    unsigned char* ext;                             // [B * H][row_tiles][kDenseExt]
     float* dlam_part;                               // [H][B][query_tiles] sums of delta_2
     unsigned* dlam_done;                            // [H] how many of a head's are there
     unsigned long long wait_ns;
@@ -828,6 +844,24 @@ __global__ void __launch_bounds__(256) dense_rows_kernel(const __grid_constant__
             row[64] = some ? kDenseShift<T> - l2 * 1.4426950408889634f : -INFINITY;
             row[128] = -fmaf(lam, d2, d1) * kDenseUnshift<T>;
             row[192] = -d2 * kDenseUnshift<T>;
+            row[256] = fmaf(lam, d2, d1) - d2;
+            unsigned char* e = f.ext + (static_cast<long long>(bh) * f.row_tiles + t) * kDenseExt;
+            const float v[3] = {row[0] / a.scale_log2, row[64] / a.scale_log2, -fmaf(lam, d2, d1)};
+#pragma unroll
+            for (int z = 0; z < 4; ++z) {
+                uint4 w = make_uint4(0, 0, 0, 0);
+                if (z < 3) {
+                    const float x = v[z];
+                    const float w0 = dense_ext_weight<T>(0), w1 = dense_ext_weight<T>(1), w2 = dense_ext_weight<T>(2);
+                    const T p0 = from_f<T>(x / w0);
+                    const float r1 = isinf(x) ? 0.f : x - to_f<T>(p0) * w0;
+                    const T p1 = from_f<T>(r1 / w1);
+                    w.x = pack2<T>(to_f<T>(p0), to_f<T>(p1));
+                    w.y = pack2<T>((r1 - to_f<T>(p1) * w1) / w2, 0.f);
+                }
+                *reinterpret_cast<uint4*>(e + sw128(c, 2 * z)) = w;
+                *reinterpret_cast<uint4*>(e + sw128(c, 2 * z + 1)) = make_uint4(0, 0, 0, 0);
+            }
         }
     }
 }
@@ -845,7 +879,8 @@ __global__ void __launch_bounds__(256) dense_rows_kernel(const __grid_constant__
 // X and Y are A operands too: for queries they lie in tensor memory beside the
 // accumulators, and the products run at full rate (32 cycles a step of 16, where
 // both from shared memory, as for keys, take 48: its bandwidth is the bound there,
-// about 1800 cycles a tile with the loads, dS_2 and the row values).
+// with the loads and dS_2; the row values as an operand took 2048 tokens with
+// their forward from 360 to 350 us, 4 x 1531 ragged ones from 212 to 202).
 // S(i+1) is issued once both warpgroups have read S(i) into registers, and runs
 // while they form the weights of tile i: a warpgroup takes 32 of the 64 columns.
 // The queries also sum P_2 (.) dP, which is delta_2 without the rounding of out2:
@@ -858,10 +893,11 @@ struct DenseBwdLayout {
     static constexpr int RBOX = 128 * 128, SBOX = 64 * 128;   // 64 columns of 128 / 64 rows
     static constexpr int RES = 128 * D * 2;                    // a resident tile
     static constexpr int STR = 64 * D * 2;                     // a streamed tile
-    static constexpr int STAGE = 2 * STR + 1024;               // x, y, row values
-    static constexpr int SLOTS = D == 128 ? 4 : 6;
+    static constexpr int STAGE = 2 * STR + kDenseExt + 1024;   // x, y, keys: the rows' values as an operand and as such
+    static constexpr int SLOTS = D == 128 ? 3 : 5;
     static constexpr int OFF_DS2 = 2 * RES;                    // keys: dS_2, 128 rows of 64 values
-    static constexpr int OFF_RING = OFF_DS2 + 16384;
+    static constexpr int OFF_ONE = OFF_DS2 + 16384;            // keys: 128 rows of 128 bytes, the parts' weights, zeros
+    static constexpr int OFF_RING = OFF_ONE + 16384;
     static constexpr int OFF_MISC = OFF_RING + SLOTS * STAGE;
     static constexpr int SMEM = 1024 + OFF_MISC + 256;
     static_assert(SMEM <= 232448, "shared memory of an SM");
@@ -945,6 +981,14 @@ __device__ __forceinline__ void dense_bwd_cta(const DenseBwdMaps& tm, const Dens
         tmem_alloc(tmem_slot, 512);
         tmem_relinquish();
     }
+    if (KEYS) {
+        for (int x = tid; x < 1024; x += kDenseThreads) {
+            const uint32_t w = pack2<T>(dense_ext_weight<T>(0), dense_ext_weight<T>(1)), w2 = pack2<T>(dense_ext_weight<T>(2), 0.f);
+            *reinterpret_cast<uint4*>(smem + L::OFF_ONE + sw128(x >> 3, x & 7)) =
+                x & 7 ? make_uint4(0, 0, 0, 0) : make_uint4(w, w2, 0, 0);
+        }
+        fence_proxy_async_smem();
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -982,16 +1026,17 @@ __device__ __forceinline__ void dense_bwd_cta(const DenseBwdMaps& tm, const Dens
             if (leader) {
                 unsigned char* st = smem + L::OFF_RING + rp.slot * L::STAGE;
                 uint64_t* bar = &full[rp.slot];
-                mbar_arrive_expect_tx(bar, 2 * L::STR + (KEYS ? kDenseRowFloats * 4 : 0));
+                mbar_arrive_expect_tx(bar, 2 * L::STR + (KEYS ? kDenseExt + 256 : 0));
                 const int xh = h * (KEYS ? f.q_h : f.k_h), yh = h * (KEYS ? f.do_h : f.v_h);
                 for (int c = 0; c < NBOX; ++c) {
                     tma_load_4d(st + c * L::SBOX, mx, bar, c * 64, t * 64, xh, xb);
                     tma_load_4d(st + L::STR + c * L::SBOX, my, bar, c * 64, t * 64, yh, yb);
                 }
-                if (KEYS)
-                    bulk_load(st + 2 * L::STR,
-                              f.rowdata + ((static_cast<long long>(b) * a.H + h) * f.row_tiles + t) * kDenseRowFloats,
-                              kDenseRowFloats * 4, bar);
+                if (KEYS) {
+                    const long long at = (static_cast<long long>(b) * a.H + h) * f.row_tiles + t;
+                    bulk_load(st + 2 * L::STR, f.ext + at * kDenseExt, kDenseExt, bar);
+                    bulk_load(st + 2 * L::STR + kDenseExt, f.rowdata + at * kDenseRowFloats + 256, 256, bar);
+                }
             }
             __syncwarp();
             rp.step(1);
@@ -1007,7 +1052,8 @@ __device__ __forceinline__ void dense_bwd_cta(const DenseBwdMaps& tm, const Dens
         constexpr int STEPS = D / 32;
         const bool leader = elect_one();
         const uint64_t X0 = sdesc(sbase, 16, 1024, kSwizzle128B), Y0 = sdesc(sbase + L::RES, 16, 1024, kSwizzle128B),
-                       x0 = sdesc(sbase + L::OFF_RING, 16, 1024, kSwizzle128B);
+                       x0 = sdesc(sbase + L::OFF_RING, 16, 1024, kSwizzle128B),
+                       one = sdesc(sbase + L::OFF_ONE, 16, 1024, kSwizzle128B);
         RingPos<SLOTS> rp{0, 0u};
         bool ok = n == 0 || wait(r_full, 0);
         for (int i = 0; ok && i < n; ++i) {
@@ -1015,7 +1061,7 @@ __device__ __forceinline__ void dense_bwd_cta(const DenseBwdMaps& tm, const Dens
             if (i > 0 && !(ok = wait(s_free, (i - 1) & 1))) break;
             tc_fence_after();
             if (leader) {
-                const uint64_t xd = x0 + rp.slot * (L::STAGE >> 4), yd = xd + (L::STR >> 4);
+                const uint64_t xd = x0 + rp.slot * (L::STAGE >> 4), yd = xd + (L::STR >> 4), ed = yd + (L::STR >> 4);
 #pragma unroll
                 for (int kk = 0; kk < 2 * STEPS; ++kk) {
                     const uint64_t bd = xd + (((kk >> 2) * L::SBOX + (kk & 3) * 32) >> 4);
@@ -1033,6 +1079,9 @@ __device__ __forceinline__ void dense_bwd_cta(const DenseBwdMaps& tm, const Dens
                     else
                         umma_f16_ts(tmem + COL_DP, tmem + COL_Y + kk * 8, bd, ID_S, kk ? 1u : 0u);
                 }
+                if (KEYS)      // - lse_1, - lse_2, - delta_1 of the columns
+#pragma unroll
+                    for (int z = 0; z < 3; ++z) umma_f16_ss(tmem + z * 64, one, ed + z * 2, ID_S, 1u);
                 umma_commit(s_full);
             }
             __syncwarp();
@@ -1146,40 +1195,39 @@ __device__ __forceinline__ void dense_bwd_cta(const DenseBwdMaps& tm, const Dens
             }
             const uint64_t nlam2 = f2pack(-lam, -lam);
             unsigned char* st = smem + L::OFF_RING + rp.slot * L::STAGE;
-            const float* rd = reinterpret_cast<const float*>(st + 2 * L::STR) + w * 32;
+            // keys: S and dP hold - lse and - delta_1 already; delta_1 - delta_2 of the columns is read here
+            const float* rd = reinterpret_cast<const float*>(st + 2 * L::STR + kDenseExt) + w * 32;
             uint32_t ww[16], d1[16], d2[16];
 #pragma unroll
             for (int x = 0; x < 8; ++x) {
-                uint64_t l1[2], l2[2], e1[2], e2[2];
+                uint64_t dd[2] = {0, 0};
                 if (KEYS) {
                     const ulonglong2 u1 = *reinterpret_cast<const ulonglong2*>(rd + 4 * x);
-                    const ulonglong2 u2 = *reinterpret_cast<const ulonglong2*>(rd + 64 + 4 * x);
-                    const ulonglong2 u3 = *reinterpret_cast<const ulonglong2*>(rd + 128 + 4 * x);
-                    const ulonglong2 u4 = *reinterpret_cast<const ulonglong2*>(rd + 192 + 4 * x);
-                    l1[0] = u1.x, l1[1] = u1.y, l2[0] = u2.x, l2[1] = u2.y;
-                    e1[0] = u3.x, e1[1] = u3.y, e2[0] = u4.x, e2[1] = u4.y;
-                } else {
-                    l1[0] = l1[1] = nl1, l2[0] = l2[1] = nl2, e1[0] = e1[1] = nd1, e2[0] = e2[1] = nd2;
+                    dd[0] = u1.x, dd[1] = u1.y;
                 }
 #pragma unroll
                 for (int z = 0; z < 2; ++z) {
                     const int y = 2 * x + z, k = 2 * y;
                     float u, v;
-                    const uint64_t x1 = ffma2(f2pack(__uint_as_float(s1[k]), __uint_as_float(s1[k + 1])), c2, l1[z]);
-                    const uint64_t x2 = ffma2(f2pack(__uint_as_float(s2[k]), __uint_as_float(s2[k + 1])), c2, l2[z]);
-                    const uint64_t p1 = exp2_2(x1), q2 = exp2_2(x2);
-                    const uint64_t g = f2pack(__uint_as_float(dp[k]), __uint_as_float(dp[k + 1]));
-                    if (!KEYS) delta2 = ffma2(q2, g, delta2);
-                    f2unpack(fmul2(p1, ffma2(g, un2, e1[z])), u, v);
-                    d1[y] = pack2<T>(u, v);
+                    const uint64_t z1 = f2pack(__uint_as_float(s1[k]), __uint_as_float(s1[k + 1])),
+                                   z2 = f2pack(__uint_as_float(s2[k]), __uint_as_float(s2[k + 1])),
+                                   g = f2pack(__uint_as_float(dp[k]), __uint_as_float(dp[k + 1]));
                     if (KEYS) {
-                        const uint64_t p2 = fmul2(q2, nlam2);          // -lambda P_2
-                        f2unpack(fmul2(p2, ffma2(g, un2, e2[z])), u, v);
+                        const uint64_t p1 = exp2_2(fmul2(z1, c2)), p2 = fmul2(exp2_2(fmul2(z2, c2)), nlam2);   // P_1, -lambda P_2
+                        uint64_t w1 = fmul2(p1, g), w2 = fmul2(p2, fadd2(g, dd[z]));
+                        if (kDenseUnshift<T> != 1.f) w1 = fmul2(w1, un2), w2 = fmul2(w2, un2);
+                        f2unpack(w1, u, v);
+                        d1[y] = pack2<T>(u, v);
+                        f2unpack(w2, u, v);
                         d2[y] = pack2<T>(u, v);
                         f2unpack(fadd2(p1, p2), u, v);
                         ww[y] = pack2<T>(u, v);
                     } else {                                           // (dq_2 takes -lambda in the end)
-                        f2unpack(fmul2(q2, ffma2(g, un2, e2[z])), u, v);
+                        const uint64_t p1 = exp2_2(ffma2(z1, c2, nl1)), p2 = exp2_2(ffma2(z2, c2, nl2));
+                        delta2 = ffma2(p2, g, delta2);
+                        f2unpack(fmul2(p1, ffma2(g, un2, nd1)), u, v);
+                        d1[y] = pack2<T>(u, v);
+                        f2unpack(fmul2(p2, ffma2(g, un2, nd2)), u, v);
                         d2[y] = pack2<T>(u, v);
                     }
                 }

@@ -94,7 +94,7 @@ DensePlan dense_plan(const sla_dense_params_t* p) {
 }
 
 struct DenseWs {
-    size_t rowdata, dlam_part, dlam_done, opart, lpart, total;
+    size_t rowdata, ext, dlam_part, dlam_done, opart, lpart, total;
 };
 
 DenseWs dense_layout(const sla_dense_params_t* p) {
@@ -114,6 +114,7 @@ DenseWs dense_layout(const sla_dense_params_t* p) {
     if (p->differential) {
         const size_t tiles = static_cast<size_t>(p->B) * p->H * ((p->Nq + sla::kDenseRowTile - 1) / sla::kDenseRowTile);
         w.rowdata = take(tiles * sla::kDenseRowFloats * 4);
+        w.ext = take(tiles * sla::kDenseExt);
         w.dlam_part = take(tiles * 4);         // (a place for each 128 queries; one for each 64 are enough)
         w.dlam_done = take(static_cast<size_t>(p->H) * 4);
     }
@@ -255,7 +256,7 @@ sla_status_t dense_bwd(const sla_dense_params_t* p, const sla::DenseArgs& a, voi
     f.query_tiles = (p->Nq + 127) / 128;
     f.row_tiles = (p->Nq + sla::kDenseRowTile - 1) / sla::kDenseRowTile;
     f.key_items = p->B * p->Hk * f.key_tiles;
-    f.rowdata = at<float>(ws, w.rowdata), f.dlam_part = at<float>(ws, w.dlam_part), f.dlam_done = at<unsigned>(ws, w.dlam_done);
+    f.rowdata = at<float>(ws, w.rowdata), f.ext = at<unsigned char>(ws, w.ext), f.dlam_part = at<float>(ws, w.dlam_part), f.dlam_done = at<unsigned>(ws, w.dlam_done);
     f.wait_ns = wait_limit_ns();
     f.debug_stall = debug_stall() ? 1 : 0;
     sla::DenseBwdMaps tm{};
@@ -337,6 +338,9 @@ extern "C" sla_status_t sla_diff_backward(const sla_dense_params_t* p, const int
     if (p->Nk && ((s = check_tensor(k, 16)) || (s = check_tensor(v, 16)) || (s = check_tensor(dk, 16)) ||
                   (s = check_tensor(dv, 16))))
         return s;
+    // (a scale at which log-sum-exps over it leave the range of the kernel's parts: 2^-20, 2^-100)
+    if (p->sm_scale > 0.f && p->sm_scale < (p->io_dtype == SLA_IO_FP16 ? 9.5367431640625e-7f : 7.888609e-31f))
+        return SLA_ERR_UNSUPPORTED;
     // (broadcast keys of a size that no gradient has room for)
     if (static_cast<long long>(p->B) * p->Hk * ((p->Nk + 127) / 128) > (1LL << 30)) return SLA_ERR_UNSUPPORTED;
     sla::DenseArgs a{};

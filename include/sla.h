@@ -379,6 +379,8 @@ sla_status_t sla_diff_forward(const sla_dense_params_t *p, const int64_t *stride
  *   dq_m = dS_m k_m,  dk_m = dS_m^T q_m,  dlambda_h = -sum delta_2
  * dk and dv are summed over the query heads that share a key/value head, and
  * dlambda over batch and queries.  Rows of dout at padding queries are not read.
+ * tau must be >= 2^-20 (fp16) or 2^-100 (bf16); fp16 takes |q.k| and |delta| up to
+ * 2^29.
  * strides: 24 values, of q, k, v, out, dout, dq, dk, dv.
  */
 sla_status_t sla_diff_backward(const sla_dense_params_t *p, const int64_t *strides, const void *q,

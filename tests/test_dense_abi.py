@@ -72,6 +72,13 @@ def test_gradients_of_more_keys_than_memory_has_room_for(lib):
     assert bwd(lib, p, st=st) == UNSUPPORTED
 
 
+def test_gradients_of_a_scale_beyond_range(lib):
+    assert bwd(lib, pd(io_dtype=S.SLA_IO_FP16, sm_scale=2.0 ** -21), n=0) == UNSUPPORTED
+    assert bwd(lib, pd(io_dtype=S.SLA_IO_FP16, sm_scale=2.0 ** -20), n=0) == WORKSPACE
+    assert bwd(lib, pd(sm_scale=2.0 ** -99), n=0) == WORKSPACE
+    assert bwd(lib, pd(sm_scale=2.0 ** -101), n=0) == UNSUPPORTED
+
+
 def test_null_parameters_and_flags(lib):
     assert lib.sla_dense_workspace_size(None) == 0
     assert lib.sla_diff_forward(None, None, *[FAKE] * 10, BIG, None) == INVALID

@@ -134,6 +134,25 @@ BWD = [
 ]
 
 
+@pytest.mark.parametrize("dt,scale", [("fp16", 2.0 ** -20), ("fp16", 2.0), ("bf16", 2.0 ** -30), ("bf16", 3.0),
+                                      ("fp16", 0.01)])
+def test_diff_backward_at_scales(dt, scale):
+    x = make(1, 2, 1, 150, 200, 64, dt, grads=True, std=0.3)
+    r = backward(x, forward(x, True, sm_scale=scale))
+    ok()
+    R.check(r, R.dense(**x, causal=True, sm_scale=scale), ("out", "dq", "dk", "dv", "dlam"))
+
+
+@pytest.mark.parametrize("gain", [2.0 ** -12, 2.0 ** 6])
+def test_diff_backward_of_small_and_large_gradients(gain):
+    """fp16 with dout far from 1: delta reaches some 2^-9 and 2^10, results stay below 65504."""
+    x = make(1, 2, 1, 150, 200, 64, "fp16", grads=True, std=0.3)
+    x["dout"] = (x["dout"].float() * gain).half()
+    r = backward(x, forward(x, True))
+    ok()
+    R.check(r, R.dense(**x, causal=True), ("out", "dq", "dk", "dv", "dlam"))
+
+
 @pytest.mark.parametrize("c", BWD, ids=lambda c: "-".join(map(str, c[:8])))
 def test_diff_backward(c):
     B, H, Hk, Nq, Nk, d, dt, causal, ql, kl = c
