@@ -873,14 +873,15 @@ __global__ void __launch_bounds__(256) dense_rows_kernel(const __grid_constant__
 // so no sums cross CTAs and the gradients are the same bits every time.  In both
 // the tile is held with the resident row in the tensor-memory lane (for keys
 // that is S^T), so W and dS, written by the thread of their row in 16 bits, are
-// the A operands of the accumulating products: W and dS_1 from tensor memory;
-// dS_2 from shared memory for keys, whose accumulators leave no columns for it.
+// the A operands of the accumulating products: from tensor memory, but dS_2 of the
+// keys for d = 128, whose accumulators leave no columns for it, from shared memory.
 //   S_m = X_m x_m^T, dP = Y y^T      tcgen05 M = 128, N = 64
 // X and Y are A operands too: for queries they lie in tensor memory beside the
 // accumulators, and the products run at full rate (32 cycles a step of 16, where
 // both from shared memory, as for keys, take 48: its bandwidth is the bound there,
-// with the loads and dS_2; the row values as an operand took 2048 tokens with
-// their forward from 360 to 350 us, 4 x 1531 ragged ones from 212 to 202).
+// with the loads and dS_2; the row values as an operand took 2 x 2048 tokens, d =
+// 128, with their forward from 361 to 353 us, 4 x 1531 ragged ones, d = 64, from
+// 211 to 203, and K and dS_2 in tensor memory, which d = 64 has room for, to 196).
 // S(i+1) is issued once both warpgroups have read S(i) into registers, and runs
 // while they form the weights of tile i: a warpgroup takes 32 of the 64 columns.
 // The queries also sum P_2 (.) dP, which is delta_2 without the rounding of out2:
@@ -925,6 +926,9 @@ __device__ __forceinline__ void dense_bwd_cta(const DenseBwdMaps& tm, const Dens
     // accumulators: keys dv first; then dk or dq: for d = 128 one of D columns (map m in its half), for d = 64
     // one for each map over all 64 columns of x, of which its half is the result (N = 64 either way)
     constexpr uint32_t COL_G = COL_ACC + (KEYS ? D : 0);
+    // d = 64 leaves the keys columns behind their accumulators: for dS_2, and for K, then the A operand of S
+    constexpr bool ROOM = KEYS && D == 64;
+    constexpr uint32_t COL_DS2 = KEYS ? 448 : COL_W, COL_K = 480;
     const uint32_t sbase = smem_u32(smem);
     const DenseArgs& a = f.a;
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::OFF_MISC);   // [SLOTS]
@@ -968,7 +972,7 @@ __device__ __forceinline__ void dense_bwd_cta(const DenseBwdMaps& tm, const Dens
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
         }
-        mbar_init(r_full, KEYS ? 1 : 8);
+        mbar_init(r_full, ROOM ? 5 : KEYS ? 1 : 8);
         mbar_init(s_full, 1);
         mbar_init(s_free, 8);
         mbar_init(p_full, 8);
@@ -1007,11 +1011,12 @@ __device__ __forceinline__ void dense_bwd_cta(const DenseBwdMaps& tm, const Dens
         const CUtensorMap *mx = KEYS ? &tm.q : &tm.k, *my = KEYS ? &tm.dout : &tm.v;
         const int n_load = f.debug_stall ? 0 : n;
         if (KEYS && n_load > 0 && leader) {
-            mbar_arrive_expect_tx(r_full, 2 * L::RES);
+            mbar_arrive_expect_tx(r_full, (ROOM ? 1 : 2) * L::RES);
             for (int c = 0; c < NBOX; ++c)
                 for (int z = 0; z < 2; ++z) {
-                    tma_load_4d(smem + c * L::RBOX + z * L::SBOX, &tm.k, r_full, c * 64, row0 + z * 64, hr * f.k_h,
-                                b * f.k_b);
+                    if (!ROOM)
+                        tma_load_4d(smem + c * L::RBOX + z * L::SBOX, &tm.k, r_full, c * 64, row0 + z * 64, hr * f.k_h,
+                                    b * f.k_b);
                     tma_load_4d(smem + L::RES + c * L::RBOX + z * L::SBOX, &tm.v, r_full, c * 64, row0 + z * 64,
                                 hr * f.v_h, b * f.v_b);
                 }
@@ -1044,7 +1049,7 @@ __device__ __forceinline__ void dense_bwd_cta(const DenseBwdMaps& tm, const Dens
         }
         if (!ok) fail();
         // every load has landed before the CTA exits
-        if (KEYS && n_load > 0) mbar_wait(r_full, 0, abort_flag, drain_lim);
+        if (KEYS && n_load > 0) mbar_wait(r_full, 0, abort_flag, drain_lim);   // (with the warps' own arrivals)
         for (int y = max(0, i - SLOTS); y < i; ++y) mbar_wait(&full[y % SLOTS], (y / SLOTS) & 1, abort_flag, drain_lim);
     } else if (warp == 1) {
         // ==================================================== issuer of S and dP
@@ -1065,11 +1070,12 @@ __device__ __forceinline__ void dense_bwd_cta(const DenseBwdMaps& tm, const Dens
 #pragma unroll
                 for (int kk = 0; kk < 2 * STEPS; ++kk) {
                     const uint64_t bd = xd + (((kk >> 2) * L::SBOX + (kk & 3) * 32) >> 4);
-                    if (KEYS)
+                    if (KEYS && !ROOM)
                         umma_f16_ss(tmem + (kk / STEPS) * 64, X0 + (((kk >> 2) * L::RBOX + (kk & 3) * 32) >> 4), bd, ID_S,
                                     kk % STEPS ? 1u : 0u);
                     else
-                        umma_f16_ts(tmem + (kk / STEPS) * 64, tmem + COL_X + kk * 8, bd, ID_S, kk % STEPS ? 1u : 0u);
+                        umma_f16_ts(tmem + (kk / STEPS) * 64, tmem + (KEYS ? COL_K : COL_X) + kk * 8, bd, ID_S,
+                                    kk % STEPS ? 1u : 0u);
                 }
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
@@ -1109,10 +1115,10 @@ __device__ __forceinline__ void dense_bwd_cta(const DenseBwdMaps& tm, const Dens
                     const uint64_t x1 = xd + ((k * 2048) >> 4), x2 = x1 + (D == 128 ? L::SBOX >> 4 : 0);
                     if (KEYS) umma_f16_ts(tmem + COL_ACC, tmem + COL_W + k * 8, yd + ((k * 2048) >> 4), ID_V, acc);
                     umma_f16_ts(tmem + COL_G, tmem + COL_DS1 + k * 8, x1, ID_G, acc);
-                    if (KEYS)
+                    if (KEYS && !ROOM)
                         umma_f16_ss(tmem + COL_G + 64, ds2 + ((k * 32) >> 4), x2, ID_G, acc);
                     else
-                        umma_f16_ts(tmem + COL_G + 64, tmem + COL_W + k * 8, x2, ID_G, acc);
+                        umma_f16_ts(tmem + COL_G + 64, tmem + COL_DS2 + k * 8, x2, ID_G, acc);
                 }
                 umma_commit(p_free);
                 umma_commit(&empty[rp.slot]);
@@ -1128,19 +1134,20 @@ __device__ __forceinline__ void dense_bwd_cta(const DenseBwdMaps& tm, const Dens
         const int q4 = warp & 3, w = (warp - 4) >> 2, r = q4 * 32 + lane;
         const uint32_t tl = tmem + (static_cast<uint32_t>(q4 * 32) << 16);
         const int row = row0 + r;
-        if (!KEYS && n > 0) {
-            // the resident rows to tensor memory: queries (w = 0) and dout (w = 1), zeros for padding
-            const T* src = static_cast<const T*>(w ? a.dout : a.q) +
-                           (row < qn ? (w ? a.dos.at(b, hr, row) : a.qs.at(b, hr, row)) : 0);
+        if ((ROOM ? w == 0 : !KEYS) && n > 0) {
+            // the resident rows to tensor memory: queries (w = 0) and dout (w = 1), or keys; zeros for padding
+            const bool have = row < (KEYS ? kn : qn);
+            const T* src = static_cast<const T*>(KEYS ? a.k : w ? a.dout : a.q) +
+                           (!have ? 0 : KEYS ? a.ks.at(b, hr, row) : w ? a.dos.at(b, hr, row) : a.qs.at(b, hr, row));
 #pragma unroll
             for (int x = 0; x < NBOX; ++x) {
                 uint32_t v[32];
 #pragma unroll
                 for (int y = 0; y < 8; ++y) {
-                    const uint4 u = row < qn ? __ldg(reinterpret_cast<const uint4*>(src + x * 64) + y) : make_uint4(0, 0, 0, 0);
+                    const uint4 u = have ? __ldg(reinterpret_cast<const uint4*>(src + x * 64) + y) : make_uint4(0, 0, 0, 0);
                     v[4 * y] = u.x, v[4 * y + 1] = u.y, v[4 * y + 2] = u.z, v[4 * y + 3] = u.w;
                 }
-                tmem_st32(tl + (w ? COL_Y : COL_X) + x * 32, v);
+                tmem_st32(tl + (KEYS ? COL_K : w ? COL_Y : COL_X) + x * 32, v);
             }
             tmem_st_wait();
             tc_fence_before();
@@ -1238,14 +1245,14 @@ __device__ __forceinline__ void dense_bwd_cta(const DenseBwdMaps& tm, const Dens
                 tc_fence_after();
             }
             tmem_st16(tl + COL_DS1 + w * 16, d1);
-            if (KEYS) {
-                tmem_st16(tl + COL_W + w * 16, ww);
+            if (KEYS) tmem_st16(tl + COL_W + w * 16, ww);
+            if (KEYS && !ROOM) {
 #pragma unroll
                 for (int y = 0; y < 4; ++y)
                     *reinterpret_cast<uint4*>(smem + L::OFF_DS2 + sw128(r, w * 4 + y)) =
                         make_uint4(d2[4 * y], d2[4 * y + 1], d2[4 * y + 2], d2[4 * y + 3]);
             } else {
-                tmem_st16(tl + COL_W + w * 16, d2);
+                tmem_st16(tl + COL_DS2 + w * 16, d2);
             }
             if (t == dirty) {      // rows past the length to zero: they are B operands of the products below
                 if (!KEYS && !(ok = wait(&full[rp.slot], rp.phase))) break;
@@ -1255,7 +1262,7 @@ __device__ __forceinline__ void dense_bwd_cta(const DenseBwdMaps& tm, const Dens
                     for (int bx = 0; bx < 2 * NBOX; ++bx)
                         *reinterpret_cast<uint4*>(st + bx * L::SBOX + rz * 128 + y * 16) = make_uint4(0, 0, 0, 0);
             }
-            if (KEYS || t == dirty) fence_proxy_async_smem();
+            if ((KEYS && !ROOM) || t == dirty) fence_proxy_async_smem();
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
