@@ -70,7 +70,9 @@ __device__ __forceinline__ int dense_len(const int32_t* len, int b, int most) {
 // (in issue order, so S_s(u+1) may overwrite P_s(u), and S_s(u+1) complete means
 // that O_s holds tile u).  A row rescales O_s only when its maximum has grown by
 // 2^8 (P stays below 2^8, exact in the sum; the reference maximum cancels in
-// O / l).  The bound is the special function unit (8 cycles a warp and ex2, 2048
+// O / l).  fp16 weights are lifted by a further 2^7, so that they fill the type's
+// range: beside a dominating key the many others' 2^-25 would be 0 in the product,
+// though not in l.  The bound is the special function unit (8 cycles a warp and ex2, 2048
 // for a tile of both streams) beside the tensor core (1536, plain 2048).
 // Measured against this form on the 10400-token differential forward, 1.04 ms:
 // one issuing warp for both streams 1.08, 64-key tiles with two buffers of S
@@ -192,6 +194,9 @@ __device__ __forceinline__ uint64_t exp2_2(uint64_t x) {
     f2unpack(x, a, b);
     return f2pack(fast_exp2(a), fast_exp2(b));
 }
+// The streams' weights are P 2^lift: to 2^15 of fp16's 65504, and down to 2^-31.
+template <typename T>
+constexpr float kDenseLift = std::is_same<T, __half>::value ? 7.f : 0.f;
 // Own keys that query i of a sequence sees: [0, this).
 __device__ __forceinline__ int dense_own(int i, int qn, int kn, int causal) {
     return causal ? min(kn, max(0, i + kn - qn + 1)) : kn;
@@ -513,7 +518,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
             }
             if (every) turn_wait(my_turn);
             if (ok) {
-                const float nm = m == -INFINITY ? 0.f : -m * c;
+                const float nm = m == -INFINITY ? 0.f : fmaf(-m, c, kDenseLift<T>);
                 const uint64_t c2 = f2pack(c, c), nm2 = f2pack(nm, nm);
                 uint64_t sum0 = 0, sum1 = 0;
 #pragma unroll
@@ -554,7 +559,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
         const int b = me.b, lr = me.lr, qi = me.qi, h = me.h;
         const bool in = me.in, real = me.real;
         if (!real || m == -INFINITY) l = 0.f;
-        const float lse2 = l > 0.f ? m * c + log2f(l) : -INFINITY;
+        const float lse2 = l > 0.f ? m * c + (log2f(l) - kDenseLift<T>) : -INFINITY;
         const long long prow = (static_cast<long long>(b) * a.Hk + hk) * per_seq + lr;
         constexpr int M = DIFF ? 2 : 1;
         // parts: [slot][map][row]; a plain stream of its own tiles is a slot of its own
