@@ -755,17 +755,40 @@ __global__ void __launch_bounds__(128) dense_merge_kernel(const __grid_constant_
 // ------------------------------------------------------------------ gradients
 // Rows the gradient kernel streams past its resident tile, and what it reads of
 // each query: kDenseRowFloats values for 64 queries, in the order
-//   -lse_1 log2 e + shift | -lse_2 log2 e + shift | -delta_1 2^-shift | -delta_2 2^-shift | delta_1 - delta_2
+//   -lse_1 log2 e + shift | -lse_2 log2 e + shift | -delta_1 | -delta_2 | delta_1 - delta_2
 // (-inf, 0 for padding and queries that see nothing, whose weights so become 0).
-// shift is 6 for fp16: P 2^6 keeps the weights of rows of thousands of keys out of
-// the subnormal range (2^-14), and leaves lambda room up to 1000; W = P_1 - lambda
-// P_2 enters its product scaled and dv is scaled back, dS = (P 2^6) ((dP - delta)
-// 2^-6) is not scaled.
+//
+// fp16 has 15 powers of two above 1 and 24 below, and weights of 2^-12 times
+// gradients of 2^-16 lie below those, so what is packed is scaled by powers of two
+// that place its largest possible value between 2^14 and 2^15; the results are
+// scaled back in fp32.
+//   W = P_1 - lambda P_2 by 2^shift, shift = 14 - max(0, e) with every |lambda| of
+//       the heads that share a key below 2^e;
+//   dS_1 by 2^sigma, dS_2 (which holds lambda on the key side) by 2^(sigma - e):
+//       |P (dP - delta)| <= |dout|_2 |v|_2 + |delta|, largest over what a CTA meets.
+// dense_rows_kernel leaves the largest |dout|_2 and |delta| of its 64 queries and the
+// largest |v|_2 of 128 keys (a further read of v). With the scales a step of 4 x 1531
+// ragged tokens, d = 64, takes 200 us, without 195.5; 2 x 2048, d = 128: 365 and 361.
+// bf16 has fp32's range: no scales.
 constexpr int kDenseRowTile = 64, kDenseRowFloats = 5 * kDenseRowTile;
 template <typename T>
-constexpr float kDenseShift = std::is_same<T, __half>::value ? 6.f : 0.f;
+constexpr bool kDenseScaled = std::is_same<T, __half>::value;
+// The smallest e with |x| < 2^e (-126 for 0, 129 for no finite x), and 2^e.
+__device__ __forceinline__ int exp_above(float x) { return ((__float_as_int(x) >> 23) & 255) - 126; }
+__device__ __forceinline__ float exp2_int(int e) { return __int_as_float((e + 127) << 23); }
+// The largest of a warp's values, none negative (their bits order as they do).
+__device__ __forceinline__ float warp_max(float x) {
+    return __uint_as_float(__reduce_max_sync(~0u, __float_as_uint(x)));
+}
+// This lane's largest |lambda| of a group of n heads, and e of the warp's.
 template <typename T>
-constexpr float kDenseUnshift = std::is_same<T, __half>::value ? 0.015625f : 1.f;
+__device__ __forceinline__ float dense_lam_max(const T* lam, int n, int lane) {
+    float x = 0.f;
+    for (int y = lane; y < n; y += 32) x = fmaxf(x, fabsf(to_f<T>(lam[y])));
+    return x;
+}
+__device__ __forceinline__ int dense_lam_exp(float x) { return min(17, max(-20, exp_above(warp_max(x)))); }
+__device__ __forceinline__ int dense_shift(int lam_exp) { return 14 - max(0, lam_exp); }
 
 // For the key side the same values of a tile also lie as an operand of the S and dP
 // products, 64 rows of 128 bytes in the 128-byte swizzle: elements 0-2, 16-18 and
@@ -788,6 +811,8 @@ struct DenseBwdArgs {
     int key_items, key_tiles, query_tiles;          // CTAs of 128 keys, then CTAs of 128 queries
     int row_tiles;                                  // ceil(Nq / 64)
     float* rowdata;                                 // [B * H][row_tiles][kDenseRowFloats]
+    float2* bound;                                  // fp16: [B * H][row_tiles] largest |dout|_2, largest |delta|
+    float* vnorm;                                   // fp16: [B * Hk][key_tiles] largest |v|_2
     unsigned char* ext;                             // [B * H][row_tiles][kDenseExt]
     float* dlam_part;                               // [H][B][query_tiles] sums of delta_2
     unsigned* dlam_done;                            // [H] how many of a head's are there
@@ -801,19 +826,58 @@ struct DenseBwdMaps {
 
 // The per-query values above, from one read of dout, out and out2:
 //   delta_2 = dout . out2,  delta_1 = dout . O_1 = dout . out + lambda delta_2.
-// One CTA a tile of 64 queries of a head, 8 lanes a row.
+// One CTA a tile of 64 queries of a head, 8 lanes a row; for fp16 then one a tile of
+// 128 keys of a key/value head, for its largest |v|_2.
 template <int D, typename T>
 __global__ void __launch_bounds__(256) dense_rows_kernel(const __grid_constant__ DenseBwdArgs f) {
     const DenseArgs& a = f.a;
+    const int lane8 = threadIdx.x & 7, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    __shared__ float2 most[8];
+    if (kDenseScaled<T> && blockIdx.x >= static_cast<unsigned>(a.B) * a.H * f.row_tiles) {
+        const int it = blockIdx.x - static_cast<unsigned>(a.B) * a.H * f.row_tiles;
+        const int t = it % f.key_tiles, hk = it / f.key_tiles % a.Hk, b = it / f.key_tiles / a.Hk;
+        const int kn = dense_len(a.kv_len, b, a.Nk);
+        let_next_start();
+        float x = 0.f;
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+            const int j = t * 128 + y * 32 + (threadIdx.x >> 3);
+            float sq = 0.f;
+            if (j < kn) {
+                const T* v = static_cast<const T*>(a.v) + a.vs.at(b, hk, j);
+#pragma unroll
+                for (int c = 0; c < D / 64; ++c) {
+                    float e[8];
+                    unpack8(__ldg(reinterpret_cast<const uint4*>(v + (c * 8 + lane8) * 8)), e, T{});
+#pragma unroll
+                    for (int z = 0; z < 8; ++z) sq = fmaf(e[z], e[z], sq);
+                }
+            }
+#pragma unroll
+            for (int z = 4; z; z >>= 1) sq += __shfl_xor_sync(~0u, sq, z);
+            x = fmaxf(x, sq);
+        }
+        x = warp_max(x);
+        if (lane == 0) most[warp].x = x;
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            for (int z = 1; z < 8; ++z) x = fmaxf(x, most[z].x);
+            f.vnorm[it] = sqrtf(x);
+        }
+        return;
+    }
     const int t = blockIdx.x % f.row_tiles, bh = blockIdx.x / f.row_tiles, h = bh % a.H, b = bh / a.H;
-    const int qn = dense_len(a.q_len, b, a.Nq), lane8 = threadIdx.x & 7;
+    const int qn = dense_len(a.q_len, b, a.Nq);
     const float lam = to_f<T>(static_cast<const T*>(a.lam)[h]);
     if (b == 0 && t == 0 && threadIdx.x == 0) f.dlam_done[h] = 0u;
     let_next_start();
+    const float lm = kDenseScaled<T> ? dense_lam_max(static_cast<const T*>(a.lam) + h / a.G * a.G, a.G, lane) : 0.f;
+    const float shift = kDenseScaled<T> ? static_cast<float>(dense_shift(dense_lam_exp(lm))) : 0.f;
+    float top = 0.f, topd = 0.f;
 #pragma unroll
     for (int y = 0; y < 2; ++y) {
         const int c = y * 32 + (threadIdx.x >> 3), i = t * kDenseRowTile + c;
-        float d1 = 0.f, d2 = 0.f;
+        float d1 = 0.f, d2 = 0.f, sq = 0.f;
         if (i < qn) {
             const T* g = static_cast<const T*>(a.dout) + a.dos.at(b, h, i);
             const T* o = static_cast<const T*>(a.out) + a.os.at(b, h, i);
@@ -829,6 +893,7 @@ __global__ void __launch_bounds__(256) dense_rows_kernel(const __grid_constant__
                 for (int z = 0; z < 8; ++z) {
                     d1 = fmaf(gv[z], ov[z], d1);
                     d2 = fmaf(gv[z], o2v[z], d2);
+                    if (kDenseScaled<T>) sq = fmaf(gv[z], gv[z], sq);
                 }
             }
         }
@@ -836,7 +901,9 @@ __global__ void __launch_bounds__(256) dense_rows_kernel(const __grid_constant__
         for (int x = 4; x; x >>= 1) {
             d1 += __shfl_xor_sync(~0u, d1, x);
             d2 += __shfl_xor_sync(~0u, d2, x);
+            if (kDenseScaled<T>) sq += __shfl_xor_sync(~0u, sq, x);
         }
+        top = fmaxf(top, sq), topd = fmaxf(topd, fmaxf(fabsf(fmaf(lam, d2, d1)), fabsf(d2)));
         if (lane8 == 0) {
             float l1 = -INFINITY, l2 = -INFINITY;
             if (i < qn) {
@@ -845,10 +912,10 @@ __global__ void __launch_bounds__(256) dense_rows_kernel(const __grid_constant__
             }
             const bool some = l1 > -INFINITY;
             float* row = f.rowdata + (static_cast<long long>(bh) * f.row_tiles + t) * kDenseRowFloats + c;
-            row[0] = some ? kDenseShift<T> - l1 * 1.4426950408889634f : -INFINITY;
-            row[64] = some ? kDenseShift<T> - l2 * 1.4426950408889634f : -INFINITY;
-            row[128] = -fmaf(lam, d2, d1) * kDenseUnshift<T>;
-            row[192] = -d2 * kDenseUnshift<T>;
+            row[0] = some ? shift - l1 * 1.4426950408889634f : -INFINITY;
+            row[64] = some ? shift - l2 * 1.4426950408889634f : -INFINITY;
+            row[128] = -fmaf(lam, d2, d1);
+            row[192] = -d2;
             row[256] = fmaf(lam, d2, d1) - d2;
             unsigned char* e = f.ext + (static_cast<long long>(bh) * f.row_tiles + t) * kDenseExt;
             const float v[3] = {row[0] / a.scale_log2, row[64] / a.scale_log2, -fmaf(lam, d2, d1)};
@@ -867,6 +934,15 @@ __global__ void __launch_bounds__(256) dense_rows_kernel(const __grid_constant__
                 *reinterpret_cast<uint4*>(e + sw128(c, 2 * z)) = w;
                 *reinterpret_cast<uint4*>(e + sw128(c, 2 * z + 1)) = make_uint4(0, 0, 0, 0);
             }
+        }
+    }
+    if (kDenseScaled<T>) {
+        top = warp_max(top), topd = warp_max(topd);
+        if (lane == 0) most[warp] = make_float2(top, topd);
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            for (int z = 1; z < 8; ++z) top = fmaxf(top, most[z].x), topd = fmaxf(topd, most[z].y);
+            f.bound[blockIdx.x] = make_float2(sqrtf(top), topd);
         }
     }
 }
@@ -1139,6 +1215,29 @@ __device__ __forceinline__ void dense_bwd_cta(const DenseBwdMaps& tm, const Dens
         const int q4 = warp & 3, w = (warp - 4) >> 2, r = q4 * 32 + lane;
         const uint32_t tl = tmem + (static_cast<uint32_t>(q4 * 32) << 16);
         const int row = row0 + r;
+        // what the scales come from, asked for before the resident rows (after them: 205 us a step of 4 x 1531 ragged
+        // tokens, d = 64, against 200)
+        float dn = 0.f, dl = 0.f, vn = 0.f, lm = 0.f;
+        if (kDenseScaled<T> && n > 0) {
+            lm = dense_lam_max(static_cast<const T*>(a.lam) + hk * a.G, a.G, lane);
+            if (KEYS) {
+                vn = f.vnorm[(static_cast<long long>(b) * a.Hk + hr) * f.key_tiles + tile];
+#pragma unroll 4
+                for (int y = lane; y < n; y += 32) {
+                    const float2 x = f.bound[(static_cast<long long>(b) * a.H + hr * a.G + y / per) * f.row_tiles + t0 + y % per];
+                    dn = fmaxf(dn, x.x), dl = fmaxf(dl, x.y);
+                }
+            } else {
+                const int y = row0 / kDenseRowTile + (lane & 1);
+                if (y < f.row_tiles) {
+                    const float2 x = f.bound[(static_cast<long long>(b) * a.H + hr) * f.row_tiles + y];
+                    dn = x.x, dl = x.y;
+                }
+                const float* p = f.vnorm + (static_cast<long long>(b) * a.Hk + hk) * f.key_tiles;
+#pragma unroll 4
+                for (int z = lane; z < (per + 1) / 2; z += 32) vn = fmaxf(vn, p[z]);
+            }
+        }
         if ((ROOM ? w == 0 : !KEYS) && n > 0) {
             // the resident rows to tensor memory: queries (w = 0) and dout (w = 1), or keys; zeros for padding
             const bool have = row < (KEYS ? kn : qn);
@@ -1160,7 +1259,17 @@ __device__ __forceinline__ void dense_bwd_cta(const DenseBwdMaps& tm, const Dens
             if (lane == 0) mbar_arrive(r_full);
         }
         const float c = a.scale_log2;
-        const uint64_t c2 = f2pack(c, c), un2 = f2pack(kDenseUnshift<T>, kDenseUnshift<T>);
+        const T* lams = static_cast<const T*>(a.lam) + (KEYS ? hr * a.G : hr);
+        // the weights' scale 2^shift, and those of dS_1 and dS_2 (queries: one for both, lambda comes in the end)
+        int shift = 0, up1 = 0, up2 = 0;
+        if (kDenseScaled<T> && n > 0) {
+            const int e = dense_lam_exp(lm);
+            shift = dense_shift(e);
+            up1 = min(60, max(-60, 15 - exp_above(fmaf(warp_max(dn), warp_max(vn), warp_max(dl)))));
+            up2 = KEYS ? up1 - e : up1;
+        }
+        const float un1 = exp2_int(up1 - shift), un2 = exp2_int(up2 - shift);
+        const uint64_t c2 = f2pack(c, c), un12 = f2pack(un1, un1), un22 = f2pack(un2, un2);
         uint64_t nl1 = 0, nl2 = 0, nd1 = 0, nd2 = 0;          // queries: this row's values
         if (!KEYS && n > 0) {
             const int t = row >> 6;
@@ -1169,10 +1278,10 @@ __device__ __forceinline__ void dense_bwd_cta(const DenseBwdMaps& tm, const Dens
                                               kDenseRowFloats + (row & 63);
             const float v0 = have ? rd[0] : -INFINITY, v1 = have ? rd[64] : -INFINITY, v2 = have ? rd[128] : 0.f,
                         v3 = have ? rd[192] : 0.f;
-            nl1 = f2pack(v0, v0), nl2 = f2pack(v1, v1), nd1 = f2pack(v2, v2), nd2 = f2pack(v3, v3);
+            nl1 = f2pack(v0, v0), nl2 = f2pack(v1, v1);
+            nd1 = f2pack(v2 * un1, v2 * un1), nd2 = f2pack(v3 * un1, v3 * un1);
         }
         const int own = dense_own(row, qn, kn, a.causal);     // queries
-        const T* lams = static_cast<const T*>(a.lam) + (KEYS ? hr * a.G : hr);
         float lam = to_f<T>(lams[0]);
         uint64_t delta2 = 0;                                  // queries: the sum of P_2 dP, scaled as P
         RingPos<SLOTS> rp{0, 0u};
@@ -1227,7 +1336,7 @@ __device__ __forceinline__ void dense_bwd_cta(const DenseBwdMaps& tm, const Dens
                     if (KEYS) {
                         const uint64_t p1 = exp2_2(fmul2(z1, c2)), p2 = fmul2(exp2_2(fmul2(z2, c2)), nlam2);   // P_1, -lambda P_2
                         uint64_t w1 = fmul2(p1, g), w2 = fmul2(p2, fadd2(g, dd[z]));
-                        if (kDenseUnshift<T> != 1.f) w1 = fmul2(w1, un2), w2 = fmul2(w2, un2);
+                        if (kDenseScaled<T>) w1 = fmul2(w1, un12), w2 = fmul2(w2, un22);
                         f2unpack(w1, u, v);
                         d1[y] = pack2<T>(u, v);
                         f2unpack(w2, u, v);
@@ -1237,9 +1346,9 @@ __device__ __forceinline__ void dense_bwd_cta(const DenseBwdMaps& tm, const Dens
                     } else {                                           // (dq_2 takes -lambda in the end)
                         const uint64_t p1 = exp2_2(ffma2(z1, c2, nl1)), p2 = exp2_2(ffma2(z2, c2, nl2));
                         delta2 = ffma2(p2, g, delta2);
-                        f2unpack(fmul2(p1, ffma2(g, un2, nd1)), u, v);
+                        f2unpack(fmul2(p1, kDenseScaled<T> ? ffma2(g, un12, nd1) : fadd2(g, nd1)), u, v);
                         d1[y] = pack2<T>(u, v);
-                        f2unpack(fmul2(p2, ffma2(g, un2, nd2)), u, v);
+                        f2unpack(fmul2(p2, kDenseScaled<T> ? ffma2(g, un12, nd2) : fadd2(g, nd2)), u, v);
                         d2[y] = pack2<T>(u, v);
                     }
                 }
@@ -1286,12 +1395,13 @@ __device__ __forceinline__ void dense_bwd_cta(const DenseBwdMaps& tm, const Dens
         const int x0 = KEYS ? 0 : w * (D / 2), x1 = KEYS ? D : x0 + D / 2;
         const bool is_v = KEYS && w == 0;
         // (w = 1 of the queries holds the second map's half)
-        const float k = is_v ? kDenseUnshift<T> : !KEYS && w == 1 ? -lam * a.scale : a.scale;
+        const float unshift = exp2_int(-shift), down1 = a.scale * exp2_int(-up1), down2 = a.scale * exp2_int(-up2);
         T* dst = static_cast<T*>(KEYS ? (is_v ? a.dv : a.dk) : a.dq) +
                  (in ? (KEYS ? (is_v ? a.dvs.at(b, hr, row) : a.dks.at(b, hr, row)) : a.dqs.at(b, hr, row)) : 0);
 #pragma unroll 1
         for (int x = x0; x < x1; x += 32) {
             uint32_t o[32];
+            const float k = is_v ? unshift : !KEYS ? (w == 1 ? -lam * down1 : down1) : x < D / 2 ? down1 : down2;
             // d = 64: the second map's half lies in its own accumulator
             tmem_ld32(tl + (is_v ? COL_ACC : COL_G + (D == 64 && x >= 32 ? 64 : 0)) + x, o);
             tmem_ld_wait();
@@ -1311,7 +1421,7 @@ __device__ __forceinline__ void dense_bwd_cta(const DenseBwdMaps& tm, const Dens
             // places are added in one order
             float u, v;
             f2unpack(delta2, u, v);
-            float s = some ? (u + v) * kDenseUnshift<T> : 0.f;
+            float s = some ? (u + v) * unshift : 0.f;
 #pragma unroll
             for (int x = 16; x; x >>= 1) s += __shfl_xor_sync(~0u, s, x);
             if (lane == 0) part[warp - 4] = s;

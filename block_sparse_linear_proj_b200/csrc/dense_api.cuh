@@ -94,7 +94,7 @@ DensePlan dense_plan(const sla_dense_params_t* p) {
 }
 
 struct DenseWs {
-    size_t rowdata, ext, dlam_part, dlam_done, opart, lpart, total;
+    size_t rowdata, ext, dlam_part, dlam_done, bound, vnorm, opart, lpart, total;
 };
 
 DenseWs dense_layout(const sla_dense_params_t* p) {
@@ -117,6 +117,10 @@ DenseWs dense_layout(const sla_dense_params_t* p) {
         w.ext = take(tiles * sla::kDenseExt);
         w.dlam_part = take(tiles * 4);         // (a place for each 128 queries; one for each 64 are enough)
         w.dlam_done = take(static_cast<size_t>(p->H) * 4);
+        if (p->io_dtype == SLA_IO_FP16) {
+            w.bound = take(tiles * 8);
+            w.vnorm = take(static_cast<size_t>(p->B) * p->Hk * ((p->Nk + 127) / 128) * 4);
+        }
     }
     w.total = std::max<size_t>(std::max(w.total, off), kAlign);
     return w;
@@ -256,7 +260,9 @@ sla_status_t dense_bwd(const sla_dense_params_t* p, const sla::DenseArgs& a, voi
     f.query_tiles = (p->Nq + 127) / 128;
     f.row_tiles = (p->Nq + sla::kDenseRowTile - 1) / sla::kDenseRowTile;
     f.key_items = p->B * p->Hk * f.key_tiles;
-    f.rowdata = at<float>(ws, w.rowdata), f.ext = at<unsigned char>(ws, w.ext), f.dlam_part = at<float>(ws, w.dlam_part), f.dlam_done = at<unsigned>(ws, w.dlam_done);
+    f.rowdata = at<float>(ws, w.rowdata), f.ext = at<unsigned char>(ws, w.ext);
+    f.dlam_part = at<float>(ws, w.dlam_part), f.dlam_done = at<unsigned>(ws, w.dlam_done);
+    f.bound = at<float2>(ws, w.bound), f.vnorm = at<float>(ws, w.vnorm);
     f.wait_ns = wait_limit_ns();
     f.debug_stall = debug_stall() ? 1 : 0;
     sla::DenseBwdMaps tm{};
@@ -269,7 +275,8 @@ sla_status_t dense_bwd(const sla_dense_params_t* p, const sla::DenseArgs& a, voi
     static std::atomic<unsigned long long> asked{0};
     {
         Span sp(SLA_KERNEL_DENSE_BWD, st);
-        sla::dense_rows_kernel<D, T><<<p->B * p->H * f.row_tiles, 256, 0, st>>>(f);
+        const unsigned rows = static_cast<unsigned>(p->B) * p->H * f.row_tiles;
+        sla::dense_rows_kernel<D, T><<<rows + (half ? static_cast<unsigned>(f.key_items) : 0u), 256, 0, st>>>(f);
     }
     {
         Span sp(SLA_KERNEL_DENSE_BWD, st);

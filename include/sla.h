@@ -331,8 +331,8 @@ sla_status_t sla_permute_rows(const void *src, const int32_t *perm, void *dst, i
  *
  * Numerics: products on the tensor cores with fp32 accumulation; softmax
  * statistics, lse and every sum in fp32; the softmax weights and their
- * gradients enter their products in io_dtype (fp16: |lambda| and the gradients
- * of the logits must stay below 1000 and 65504).  Keys, values, queries and
+ * gradients enter their products in io_dtype (fp16: scaled by powers of two into
+ * its range, the gradients by the largest norms of dout and v).  Keys, values, queries and
  * dout that are no padding must be finite: a value that is not reaches the
  * other rows of its tile.  Results do not depend on how
  * the GPU orders its work: equal calls give equal bits.
