@@ -24,6 +24,8 @@ sla_status_t dense_check(const sla_dense_params_t* p) {
 // values, NULL for a dense tensor.  A dimension of one entry gets stride 0.
 sla_status_t dense_strides(const int64_t* st, int nd, int B, int H, int N, int d, bool output, sla::DenseT& t) {
     const long long size[3] = {nd == 3 ? B : 1, H, N};
+    t = {0, 0, 0};
+    if (N == 0) return SLA_OK;           // no entries: nothing to reach, nothing to overlap
     long long s[3] = {static_cast<long long>(H) * N * d, static_cast<long long>(N) * d, d};
     if (st)
         for (int x = 0; x < nd; ++x) s[3 - nd + x] = st[x];

@@ -43,3 +43,14 @@ def test_gradients_of_long_walks(c):
     r = backward(x, forward(x, c[7]))
     ok()
     R.check(r, R.dense(**x, causal=c[7]), GRADS)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+def test_gradients_without_keys(dt):
+    """No own keys at all: zeros, and dlambda too."""
+    x = make(3, 4, 2, 70, 0, 64, dt, grads=True)
+    r = backward(x, forward(x, True))
+    ok()
+    for n in ("out", "out2", "dq", "dlam"):
+        assert (r[n] == 0).all(), n
+    assert torch.isneginf(r["lse"]).all() and r["dk"].numel() == 0
