@@ -415,7 +415,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     const int n_cent = PISA ? (a.Nk + 63) / 64 : 0;
     const int n_total = n_exact + n_cent;
     const unsigned long long lim = a.wait_ns;
-    const unsigned long long drain_lim = 4000000000ull;
 
     auto sK = [&](int s) { return sbase + L::OFF_K + s * L::KT; };
     auto sV = [&](int s) { return sbase + L::OFF_V + s * L::VT; };
@@ -496,11 +495,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 }
             }
             // drain: every load this thread issued has landed before the CTA exits
-            mbar_wait(q_full, 0, abort_flag, drain_lim);
+            mbar_drain(q_full, 0);
             for (int e = max(0, kn - KS); e < kn; ++e)
-                mbar_wait(&k_full[e % KS], (e / KS) & 1, abort_flag, drain_lim);
+                mbar_drain(&k_full[e % KS], (e / KS) & 1);
             for (int e = max(0, vn - VS); e < vn; ++e)
-                mbar_wait(&v_full[e % VS], (e / VS) & 1, abort_flag, drain_lim);
+                mbar_drain(&v_full[e % VS], (e / VS) & 1);
         }
     } else if (warp == 1) {
         // ======================================================== S = Q K^T issuer
@@ -542,7 +541,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             if (!ok) fail();
             // drain: this thread's MMAs complete before TMEM is released
             umma_commit(drain_bar);
-            mbar_wait(drain_bar, 0, abort_flag, drain_lim);
+            mbar_drain(drain_bar, 0);
         }
     } else if (warp == 3) {
         // ======================================================== P.V / G / linear issuer
@@ -623,7 +622,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 }
             }
             umma_commit(drain2_bar);
-            mbar_wait(drain2_bar, 0, abort_flag, drain_lim);
+            mbar_drain(drain2_bar, 0);
         }
     } else if (warp == 2) {
         // ======================================================== z sums (SLA)

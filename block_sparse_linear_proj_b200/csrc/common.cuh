@@ -106,6 +106,17 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
     }
 }
 
+// Bounded wait for copies or products that this CTA has issued, before it leaves
+// shared memory or frees tensor memory.  Another role's abort does not end it:
+// what was issued completes, and would else land in the next CTA's memory.
+constexpr uint64_t kDrainNs = 4000000000ull;
+__device__ __forceinline__ void mbar_drain(uint64_t* bar, uint32_t parity) {
+    if (mbar_test(bar, parity)) return;
+    const uint64_t t0 = globaltimer_ns();
+    while (!mbar_test(bar, parity) && globaltimer_ns() - t0 <= kDrainNs) {
+    }
+}
+
 // ---------------------------------------------------------------- TMA
 __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, uint64_t* bar,
                                             int x, int y) {

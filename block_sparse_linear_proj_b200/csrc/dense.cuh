@@ -285,7 +285,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    const unsigned long long lim = f.wait_ns, drain_lim = 4000000000ull;
+    const unsigned long long lim = f.wait_ns;
     auto fail = [&]() {
         *abort_flag = 1;
         report(kStatusTimeout);
@@ -331,7 +331,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
         }
         if (!ok) fail();
         for (int y = 0; y < SLOTS; ++y)     // every load has landed before the CTA exits
-            if ((used >> y) & 1u) mbar_wait(&full[y], (last >> y) & 1u, abort_flag, drain_lim);
+            if ((used >> y) & 1u) mbar_drain(&full[y], (last >> y) & 1u);
     } else if (warp == 1 || warp == 2) {
         // ==================================================== MMA issuers (the whole warp waits, one lane issues)
         // One a stream: an issue blocks until the tensor core takes it, and a wait after it starts only then, so one
@@ -406,7 +406,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
         }
         if (!ok) fail();
         if (leader) umma_commit(o_full);   // also: every MMA has completed before tensor memory is released
-        mbar_wait(o_full, 0, abort_flag, drain_lim);
+        mbar_drain(o_full, 0);
     } else if (warp >= 4) {
         reg_inc<216>();
         // ==================================================== streams
@@ -1079,7 +1079,7 @@ __device__ __forceinline__ void dense_bwd_cta(const DenseBwdMaps& tm, const Dens
     tc_fence_after();
     wait_for_previous();                  // the row values
     const uint32_t tmem = *tmem_slot;
-    const unsigned long long lim = f.wait_ns, drain_lim = 4000000000ull;
+    const unsigned long long lim = f.wait_ns;
     auto fail = [&]() {
         *abort_flag = 1;
         report(kStatusTimeout);
@@ -1130,8 +1130,8 @@ __device__ __forceinline__ void dense_bwd_cta(const DenseBwdMaps& tm, const Dens
         }
         if (!ok) fail();
         // every load has landed before the CTA exits
-        if (KEYS && n_load > 0) mbar_wait(r_full, 0, abort_flag, drain_lim);   // (with the warps' own arrivals)
-        for (int y = max(0, i - SLOTS); y < i; ++y) mbar_wait(&full[y % SLOTS], (y / SLOTS) & 1, abort_flag, drain_lim);
+        if (KEYS && n_load > 0) mbar_drain(r_full, 0);   // (with the warps' own arrivals)
+        for (int y = max(0, i - SLOTS); y < i; ++y) mbar_drain(&full[y % SLOTS], (y / SLOTS) & 1);
     } else if (warp == 1) {
         // ==================================================== issuer of S and dP
         constexpr uint32_t ID_S = idesc_t<T>(128, 64, 0, 0);
@@ -1176,7 +1176,7 @@ __device__ __forceinline__ void dense_bwd_cta(const DenseBwdMaps& tm, const Dens
         }
         if (!ok) fail();
         if (leader) umma_commit(end_bar);      // also: every MMA has completed before tensor memory is released
-        mbar_wait(end_bar, 0, abort_flag, drain_lim);
+        mbar_drain(end_bar, 0);
     } else if (warp == 2) {
         // ==================================================== issuer of the accumulating products
         constexpr uint32_t ID_V = idesc_t<T>(128, D, 0, 1), ID_G = idesc_t<T>(128, 64, 0, 1);
@@ -1209,7 +1209,7 @@ __device__ __forceinline__ void dense_bwd_cta(const DenseBwdMaps& tm, const Dens
         }
         if (!ok) fail();
         if (leader) umma_commit(end_bar);
-        mbar_wait(end_bar, 0, abort_flag, drain_lim);
+        mbar_drain(end_bar, 0);
     } else if (warp >= 4) {
         // ==================================================== warpgroups
         const int q4 = warp & 3, w = (warp - 4) >> 2, r = q4 * 32 + lane;

@@ -166,6 +166,7 @@ __global__ void __launch_bounds__(256, 2) kv_stats_kernel(KvStatsArgs a) {
     constexpr int RPH = kKvTok / HALVES;
     const int col = tid % D, half = tid / D;
 
+    int issued = 0;                                          // thread 0: products issued
     for (int blk = 0; blk < nblk; ++blk) {
         const int stage = blk % kKvStages;
         cp_async_wait<kKvStages - 2>();
@@ -382,6 +383,7 @@ __global__ void __launch_bounds__(256, 2) kv_stats_kernel(KvStatsArgs a) {
                 }
             }
             umma_commit(mma_bar);
+            issued = blk + 1;
         }
     }
     cp_async_wait<0>();
@@ -410,6 +412,7 @@ __global__ void __launch_bounds__(256, 2) kv_stats_kernel(KvStatsArgs a) {
                                     __uint_as_float(v[x + 2]), __uint_as_float(v[x + 3]));
             }
         }
+        if (tid == 0 && *abort_flag && issued > 0) mbar_drain(mma_bar, (issued - 1) & 1);
         tc_fence_before();
         __syncthreads();
         if (warp == 0) tmem_dealloc(tmem, TCOLS);
