@@ -611,7 +611,7 @@ const char* sla_status_string(sla_status_t s) {
     return "unknown status";
 }
 
-int32_t sla_version(void) { return 200; }
+int32_t sla_version(void) { return 300; }
 
 sla_status_t sla_profile_enable(int32_t on) {
     Profiler& P = prof();
@@ -621,10 +621,15 @@ sla_status_t sla_profile_enable(int32_t on) {
 }
 
 sla_status_t sla_profile_read(double* ms_total, int64_t* launches) {
+    return sla_profile_read_kinds(SLA_KERNEL_KINDS, ms_total, launches);
+}
+
+sla_status_t sla_profile_read_kinds(int32_t n, double* ms_total, int64_t* launches) {
+    if (n < 0) return SLA_ERR_INVALID_ARG;
     Profiler& P = prof();
     std::lock_guard<std::mutex> g(P.mu);
     sla_status_t rc = SLA_OK;
-    for (int k = 0; k < SLA_KERNEL_KINDS; ++k) {
+    for (int k = 0; k < n; ++k) {
         if (ms_total) ms_total[k] = 0.0;
         if (launches) launches[k] = 0;
     }
@@ -632,8 +637,8 @@ sla_status_t sla_profile_read(double* ms_total, int64_t* launches) {
         float ms = 0.f;
         if (cudaEventSynchronize(r.b) != cudaSuccess || cudaEventElapsedTime(&ms, r.a, r.b) != cudaSuccess)
             rc = SLA_ERR_CUDA;
-        if (ms_total) ms_total[r.kind] += ms;
-        if (launches) launches[r.kind] += 1;
+        if (ms_total && r.kind < n) ms_total[r.kind] += ms;
+        if (launches && r.kind < n) launches[r.kind] += 1;
         P.pool.push_back(r.a);
         P.pool.push_back(r.b);
     }

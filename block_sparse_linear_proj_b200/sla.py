@@ -41,7 +41,7 @@ SLA_IO_FP16 = 1
 
 EXPORTED = ("sla_workspace_size", "sla_route", "sla_forward", "sla_pisa_forward",
             "sla_status_string", "sla_check_device_status", "sla_version",
-            "sla_profile_enable", "sla_profile_read", "sla_route_noalloc",
+            "sla_profile_enable", "sla_profile_read", "sla_profile_read_kinds", "sla_route_noalloc",
             "sla_cocluster", "sla_cocluster_workspace_size", "sla_permute_rows",
             "sla_forward_host", "sla_pisa_forward_host", "sla_dense_workspace_size",
             "sla_diff_forward", "sla_diff_backward", "sla_prefix_forward")
@@ -109,6 +109,8 @@ def load():
             lib.sla_profile_enable.restype = ctypes.c_int
             lib.sla_profile_read.argtypes = [P, P]
             lib.sla_profile_read.restype = ctypes.c_int
+            lib.sla_profile_read_kinds.argtypes = [ctypes.c_int32, P, P]
+            lib.sla_profile_read_kinds.restype = ctypes.c_int
             lib.sla_cocluster_workspace_size.argtypes = [PP, ctypes.c_int32]
             lib.sla_cocluster_workspace_size.restype = ctypes.c_size_t
             lib.sla_cocluster.argtypes = [PP, P, P, ctypes.c_int32, ctypes.c_int32, P, P, P, ctypes.c_size_t, P]
@@ -336,8 +338,8 @@ def sla_profile_read():
     n = len(KERNEL_KINDS)
     ms = (ctypes.c_double * n)()
     cnt = (ctypes.c_int64 * n)()
-    _raise(load().sla_profile_read(ctypes.cast(ms, ctypes.c_void_p), ctypes.cast(cnt, ctypes.c_void_p)),
-           "sla_profile_read")
+    _raise(load().sla_profile_read_kinds(n, ctypes.cast(ms, ctypes.c_void_p), ctypes.cast(cnt, ctypes.c_void_p)),
+           "sla_profile_read_kinds")
     return {KERNEL_KINDS[i]: (ms[i], cnt[i]) for i in range(n)}
 
 

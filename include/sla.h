@@ -420,10 +420,10 @@ sla_status_t sla_check_device_status(sla_stream_t stream);
  * bracketed by a pair of CUDA events recorded on its own stream (no device
  * cost; about a microsecond of host time per launch), and each forward call
  * records one more pair on the caller's stream, from its entry to the start
- * of its attention kernel (SLA_PHASE_PRE_ATTN).  sla_profile_read()
+ * of its attention kernel (SLA_PHASE_PRE_ATTN).  sla_profile_read_kinds()
  * synchronises those events and returns, per kernel kind, the summed device
  * time in milliseconds and the number of launches since the last read; it
- * then forgets them.  Host-side state only; guarded by a mutex.
+ * then forgets them, the kinds that were not asked for too.  Host-side state only; guarded by a mutex.
  */
 typedef enum {
     SLA_KERNEL_POOL = 0,        /* mean pooling of Q (and K in sla_route)      */
@@ -440,13 +440,18 @@ typedef enum {
                                    kernel (router, pre-pass and their joins)     */
     SLA_KERNEL_COCLUSTER = 10,  /* the co-clustering kernels of one call          */
     SLA_KERNEL_PERMUTE = 11,    /* row permutation (co-clustered order)           */
+    SLA_KERNEL_KINDS = 12,      /* what sla_profile_read returns: never changes   */
     SLA_KERNEL_DENSE = 12,      /* dense attention, and the join of its parts     */
     SLA_KERNEL_DENSE_BWD = 13,  /* gradients of differential attention            */
-    SLA_KERNEL_KINDS = 14
+    SLA_KERNEL_KINDS_ALL = 14   /* grows with the library                         */
 } sla_kernel_kind_t;
 
 sla_status_t sla_profile_enable(int32_t on);
-/* ms_total and launches: arrays of SLA_KERNEL_KINDS entries (either may be NULL). */
+/* The first n kinds into arrays of n entries (either may be NULL); entries past
+ * the library's last kind get 0.  n < 0: SLA_ERR_INVALID_ARG. */
+sla_status_t sla_profile_read_kinds(int32_t n, double *ms_total, int64_t *launches);
+/* The same for the first SLA_KERNEL_KINDS kinds, whatever kinds the library has
+ * besides, so that the arrays of a program that was compiled earlier are enough. */
 sla_status_t sla_profile_read(double *ms_total, int64_t *launches);
 
 /* Library version, major*10000 + minor*100 + patch. */
