@@ -113,7 +113,7 @@ DenseWs dense_layout(const sla_dense_params_t* p) {
     }
     w.total = off;
     off = 0;
-    if (p->differential) {
+    if (p->differential && p->P == 0) {        // (with a prefix no backward call can follow)
         const size_t tiles = static_cast<size_t>(p->B) * p->H * ((p->Nq + sla::kDenseRowTile - 1) / sla::kDenseRowTile);
         w.rowdata = take(tiles * sla::kDenseRowFloats * 4);
         w.ext = take(tiles * sla::kDenseExt);

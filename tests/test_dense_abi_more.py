@@ -2,12 +2,9 @@
 their sizes (no GPU is touched)."""
 import ctypes
 
-import pytest
 import torch
 
-import block_sparse_linear_proj_b200 as S
-from block_sparse_linear_proj_b200 import sla as B
-from test_dense_abi import INVALID, UNSUPPORTED, WORKSPACE, bwd, fwd, i64, lib, pd, pre  # noqa: F401
+from test_dense_abi import INVALID, WORKSPACE, bwd, fwd, i64, lib, pd, pre  # noqa: F401
 
 
 def test_no_own_keys(lib):  # noqa: F811
@@ -25,3 +22,15 @@ def test_no_own_keys(lib):  # noqa: F811
         assert bwd(lib, q, n=0, dk=None, dv=None, **none) == WORKSPACE
     # a gradient of queries still may not overlap
     assert bwd(lib, p, st=i64(*qs, *[0] * 6, *qs, *qs, 0, Nq * d, d, *[0] * 6), dk=None, dv=None, **none) == INVALID
+
+
+def test_workspace_of_a_prefix_call_holds_its_parts_only(lib):  # noqa: F811
+    """The backward call refuses a prefix, so a differential prefix call needs its parts, twice the plain call's (a
+    part a map), and nothing for gradients; without a prefix the size covers them."""
+    for kw in (dict(B=1024, H=32, Hk=8, Nq=1, Nk=128, d=128, prefix=4096), dict(B=3, H=8, Hk=2, Nq=5, Nk=0, prefix=900),
+               dict(B=2, H=4, Hk=4, Nq=300, Nk=300, prefix=500)):
+        need = {x: lib.sla_dense_workspace_size(ctypes.byref(pd(differential=x, **kw))) for x in (False, True)}
+        assert 0 < need[True] <= 2 * need[False] + 512
+        assert pre(lib, pd(**kw), n=need[True] - 1) == WORKSPACE
+    a, b = (lib.sla_dense_workspace_size(ctypes.byref(pd(B=40, H=4, Hk=4, Nq=300, Nk=300, prefix=x))) for x in (0, 1))
+    assert b == 256 and bwd(lib, pd(B=40, H=4, Hk=4, Nq=300, Nk=300), n=a - 1) == WORKSPACE
