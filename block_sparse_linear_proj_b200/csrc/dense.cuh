@@ -919,6 +919,8 @@ __global__ void __launch_bounds__(256) dense_rows_kernel(const __grid_constant__
             row[256] = fmaf(lam, d2, d1) - d2;
             unsigned char* e = f.ext + (static_cast<long long>(bh) * f.row_tiles + t) * kDenseExt;
             const float v[3] = {row[0] / a.scale_log2, row[64] / a.scale_log2, -fmaf(lam, d2, d1)};
+            if (kDenseScaled<T> && some && fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fabsf(v[2])) > 536870912.f)
+                report(kStatusRange);          // past what the parts hold
 #pragma unroll
             for (int z = 0; z < 4; ++z) {
                 uint4 w = make_uint4(0, 0, 0, 0);

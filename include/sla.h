@@ -379,8 +379,11 @@ sla_status_t sla_diff_forward(const sla_dense_params_t *p, const int64_t *stride
  *   dq_m = dS_m k_m,  dk_m = dS_m^T q_m,  dlambda_h = -sum delta_2
  * dk and dv are summed over the query heads that share a key/value head, and
  * dlambda over batch and queries.  Rows of dout at padding queries are not read.
- * tau must be >= 2^-20 (fp16) or 2^-100 (bf16); fp16 takes |q.k| and |delta| up to
- * 2^29.
+ * tau must be >= 2^-20 (fp16) or 2^-100 (bf16).  fp16 takes log-sum-exps over tau
+ * and |delta| up to 2^29; larger ones are flagged SLA_ERR_DEVICE_CHECK.  The softmax
+ * maps come from lse, so logits of size L carry a relative error of about L 2^-22.
+ * delta_m comes from the rounded out and out2: where |lambda| is large beside 1, the
+ * gradients of the first map take an error of about |lambda| roundings of O_2.
  * strides: 24 values, of q, k, v, out, dout, dq, dk, dv.
  */
 sla_status_t sla_diff_backward(const sla_dense_params_t *p, const int64_t *strides, const void *q,

@@ -5,6 +5,8 @@ import math
 import pytest
 import torch
 
+import block_sparse_linear_proj_b200 as S
+
 import dense_ref as R
 from test_gpu_dense import backward, forward, make, ok, prefix
 
@@ -112,6 +114,21 @@ def test_fp16_lambda_past_1000(d):
     r = backward(x, forward(x, True, [150, 90], [260, 131]))
     ok()
     R.check(r, R.dense(**x, q_len=[150, 90], kv_len=[260, 131], causal=True), ("out", "out2", "lse", "dq", "dk", "dv", "dlam"))
+
+
+@pytest.mark.parametrize("of,size,code", [("q", 6000.0, S.sla.SLA_ERR_DEVICE_CHECK), ("q", 4000.0, S.sla.SLA_OK),
+                                          ("v", 6000.0, S.sla.SLA_ERR_DEVICE_CHECK), ("v", 2800.0, S.sla.SLA_OK)])
+def test_fp16_log_sum_exps_and_deltas_past_their_range_are_flagged(of, size, code):
+    """2^29 = 5.4e8: 32 x 6000^2 (a map's q.k) and 64 x 6000^2 (dout.v) are past it, 32 x 4000^2 and 64 x 2800^2 not."""
+    x = make(1, 1, 1, 70, 90, 64, "fp16", grads=True)
+    for n in ("q", "k") if of == "q" else ("v", "dout"):
+        x[n] = torch.full_like(x[n], size)
+    r = forward(x, sm_scale=2.0 ** -18)
+    assert S.sla_check_device_status() == S.sla.SLA_OK
+    backward(x, r)
+    assert S.sla_check_device_status() == code
+    if code == S.sla.SLA_OK:
+        assert all(torch.isfinite(r[n]).all() for n in ("dq", "dk"))
 
 
 @pytest.mark.parametrize("diff", [False, True])
