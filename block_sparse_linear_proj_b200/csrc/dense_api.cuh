@@ -41,7 +41,8 @@ sla_status_t dense_strides(const int64_t* st, int nd, int B, int H, int N, int d
         for (int x : o) {
             if (size[x] <= 1) continue;
             if (s[x] < extent) return SLA_ERR_INVALID_ARG;
-            extent += s[x] * (size[x] - 1);
+            // (no address space has 2^60 elements; and the sum stays within 64 bits)
+            if (s[x] > (1LL << 60) / size[x] || (extent += s[x] * (size[x] - 1)) > (1LL << 60)) return SLA_ERR_INVALID_ARG;
         }
     }
     t = {s[0], s[1], s[2]};

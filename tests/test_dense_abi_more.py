@@ -34,3 +34,12 @@ def test_workspace_of_a_prefix_call_holds_its_parts_only(lib):  # noqa: F811
         assert pre(lib, pd(**kw), n=need[True] - 1) == WORKSPACE
     a, b = (lib.sla_dense_workspace_size(ctypes.byref(pd(B=40, H=4, Hk=4, Nq=300, Nk=300, prefix=x))) for x in (0, 1))
     assert b == 256 and bwd(lib, pd(B=40, H=4, Hk=4, Nq=300, Nk=300), n=a - 1) == WORKSPACE
+
+
+def test_strides_whose_extent_passes_64_bits(lib):  # noqa: F811
+    """2^29 tokens 2^35 elements apart span 2^64: no tensor, and no room below a batch stride of 2^33."""
+    p = pd(B=2, H=1, Hk=1, Nq=1, Nk=1 << 29)
+    d, big = p.d, 1 << 35
+    st = [d, 0, 0, 0, 0, d, 0, 0, d, d, 0, 0, d, 0, 0, d, 0, 0]
+    assert bwd(lib, p, st=i64(*st, 1 << 33, 0, big, 1 << 33, 0, big), n=0) == INVALID
+    assert bwd(lib, p, st=i64(*st, p.Nk * d, 0, d, p.Nk * d, 0, d), n=0) == WORKSPACE
