@@ -61,7 +61,7 @@ DensePlan dense_plan(const sla_dense_params_t* p) {
     DensePlan x{};
     const long long G = p->H / p->Hk, seq = G * p->Nq, all = seq * p->B;
     const bool diff = p->differential != 0;
-    constexpr long long SMS = 148;
+    constexpr long long SMS = 148;          // a B200's
     auto cdiv = [](long long u, long long v) { return (u + v - 1) / v; };
     const long long nP = cdiv(p->P, sla::kDenseBN), nK = cdiv(p->Nk, sla::kDenseBN);
     x.rows = all * p->Hk;
@@ -78,10 +78,14 @@ DensePlan dense_plan(const sla_dense_params_t* p) {
     const long long cb = gather && nK == 0 ? 0 : static_cast<long long>(p->B) * p->Hk * x.tiles_b,
                     cg = gather ? static_cast<long long>(p->Hk) * x.tiles_g : 0;
     const long long work = cb * tb + cg * nP;
-    // Ranges of key tiles that give each SM one CTA, of eight tiles at least where there is that much work, else two
-    // (a CTA's start, about 2.5 us, its end and the join cost as much as about that many).  More ranges, to even out
-    // sequences of different lengths, cost what they gave: 32 such caches, 1 range each 118 us, 2 and 4: 116, 6: 121.
-    const long long least = std::max<long long>(work >= 8 * SMS ? 8 : 2, cdiv(work, SMS));
+    // Ranges of key tiles that give the gathered and the own units up to one CTA an SM each, of eight tiles at least
+    // where there is that much work (a CTA's start, about 2.5 us, its end and the join cost as much as about that
+    // many), else three: a step of 257 tokens and 2 heads / 16 x 5 drafted tokens on 4099 + 333 keys took 35.0 / 20.5 us
+    // so, 37.2 / 24.2 with ranges of two tiles, 34.8 / 22.4 of four and 35.1 / 71.7 unsplit. (The join grows with the
+    // rows, which the rule does not see: 512 tokens of 8 heads, 26.0 us in two ranges, take 16.4 in one.)  More ranges,
+    // to even out sequences of different lengths, gave nothing with CTAs that each pay a start: 32 such caches, 1 range
+    // each 118 us, 2 and 4: 116, 6: 121.
+    const long long least = std::max<long long>(work >= 8 * SMS ? 8 : 3, cdiv(work, SMS));
     auto ranges = [&](long long units, long long tiles) {
         return units == 0 ? 0 : units >= SMS ? 1 : static_cast<int>(std::max<long long>(1, std::min(cdiv(tiles, least), SMS / units)));
     };

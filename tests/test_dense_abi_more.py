@@ -43,3 +43,9 @@ def test_strides_whose_extent_passes_64_bits(lib):  # noqa: F811
     st = [d, 0, 0, 0, 0, d, 0, 0, d, d, 0, 0, d, 0, 0, d, 0, 0]
     assert bwd(lib, p, st=i64(*st, 1 << 33, 0, big, 1 << 33, 0, big), n=0) == INVALID
     assert bwd(lib, p, st=i64(*st, p.Nk * d, 0, d, p.Nk * d, 0, d), n=0) == WORKSPACE
+
+
+def test_three_key_tiles_are_not_split(lib):  # noqa: F811
+    """A call in one part has no workspace beyond the least; four tiles of few rows are two ranges."""
+    a, b = (pd(B=1, H=2, Hk=2, Nq=257, Nk=n, differential=False) for n in (3 * 128, 3 * 128 + 1))
+    assert lib.sla_dense_workspace_size(ctypes.byref(a)) == 256 < lib.sla_dense_workspace_size(ctypes.byref(b))
