@@ -72,12 +72,14 @@ __device__ __forceinline__ int dense_len(const int32_t* len, int b, int most) {
 // 2^8 (P stays below 2^8, exact in the sum; the reference maximum cancels in
 // O / l).  fp16 weights are lifted by a further 2^7, so that they fill the type's
 // range: beside a dominating key the many others' 2^-25 would be 0 in the product,
-// though not in l.  The bound is the special function unit (8 cycles a warp and ex2, 2048
-// for a tile of both streams) beside the tensor core (1536, plain 2048).
-// Measured against this form on the 10400-token differential forward, 1.04 ms:
-// one issuing warp for both streams 1.08, 64-key tiles with two buffers of S
-// 1.15, with four warpgroups 1.10, and a share of the exponentials as polynomials
-// on the FMA pipe (a quarter: 1.06; three eighths: 1.13).
+// though not in l.  The bound is the special function unit (8 cycles a warp and ex2,
+// 2048 for a tile of both streams) beside the tensor core (1536, plain 2048).
+// Other forms of it, each measured once on the 10400-token differential forward when
+// this one took 1.04 ms: 64-key tiles with two buffers of S 1.15, three eighths of
+// the exponentials as polynomials on the FMA pipe 1.13.  (This one has taken 1.04 to
+// 1.13 ms on different boxes; 64-key tiles with four warpgroups, 1.10, one issuing
+// warp for both streams, 1.08, and a quarter of the exponentials as polynomials,
+// 1.06, lie within that.)
 // Rows are (query i, head g of the group) in the order i * G + g, so a causal
 // tile ends early and the heads of a group share each key tile.  Key tiles come
 // from the prefix first, then the sequence's own keys.  Where sequences have few
@@ -826,6 +828,11 @@ struct DenseBwdMaps {
 
 // The per-query values above, from one read of dout, out and out2:
 //   delta_2 = dout . out2,  delta_1 = dout . O_1 = dout . out + lambda delta_2.
+// out and out2 are rounded to 16 bits, which puts about 0.1% of bf16 gradients'
+// size on dq and dk beside the 0.24% of the roundings of dS and of the results.
+// (Unrounded deltas take the outputs in 32 bits, which the calls do not pass on, or
+// the sum of P dP over all keys before the first dS: another S, dP and exponentials
+// of every pair.)
 // One CTA a tile of 64 queries of a head, 8 lanes a row; for fp16 then one a tile of
 // 128 keys of a key/value head, for its largest |v|_2.
 template <int D, typename T>
