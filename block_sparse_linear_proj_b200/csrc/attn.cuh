@@ -495,11 +495,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 }
             }
             // drain: every load this thread issued has landed before the CTA exits
-            mbar_drain(q_full, 0);
+            mbar_drain(q_full, 0, abort_flag);
             for (int e = max(0, kn - KS); e < kn; ++e)
-                mbar_drain(&k_full[e % KS], (e / KS) & 1);
+                mbar_drain(&k_full[e % KS], (e / KS) & 1, abort_flag);
             for (int e = max(0, vn - VS); e < vn; ++e)
-                mbar_drain(&v_full[e % VS], (e / VS) & 1);
+                mbar_drain(&v_full[e % VS], (e / VS) & 1, abort_flag);
         }
     } else if (warp == 1) {
         // ======================================================== S = Q K^T issuer
@@ -541,7 +541,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             if (!ok) fail();
             // drain: this thread's MMAs complete before TMEM is released
             umma_commit(drain_bar);
-            mbar_drain(drain_bar, 0);
+            mbar_drain(drain_bar, 0, abort_flag);
         }
     } else if (warp == 3) {
         // ======================================================== P.V / G / linear issuer
@@ -622,7 +622,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 }
             }
             umma_commit(drain2_bar);
-            mbar_drain(drain2_bar, 0);
+            mbar_drain(drain2_bar, 0, abort_flag);
         }
     } else if (warp == 2) {
         // ======================================================== z sums (SLA)

@@ -108,13 +108,19 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
 
 // Bounded wait for copies or products that this CTA has issued, before it leaves
 // shared memory or frees tensor memory.  Another role's abort does not end it:
-// what was issued completes, and would else land in the next CTA's memory.
+// what was issued completes, and would else land in the next CTA's memory.  (First
+// a wait like the others, then one without the flag: in this form the block-sparse
+// kernels take up to 0.6% longer than with a wait that the flag ends, in others
+// up to 1%.)
 constexpr uint64_t kDrainNs = 4000000000ull;
-__device__ __forceinline__ void mbar_drain(uint64_t* bar, uint32_t parity) {
-    if (mbar_test(bar, parity)) return;
+__device__ __forceinline__ void mbar_drain(uint64_t* bar, uint32_t parity, volatile int* abort) {
+    if (mbar_wait(bar, parity, abort, kDrainNs)) return;
     const uint64_t t0 = globaltimer_ns();
-    while (!mbar_test(bar, parity) && globaltimer_ns() - t0 <= kDrainNs) {
-    }
+    do {
+#pragma unroll 1
+        for (int i = 0; i < 32; ++i)
+            if (mbar_test(bar, parity)) return;
+    } while (globaltimer_ns() - t0 <= kDrainNs);
 }
 
 // ---------------------------------------------------------------- TMA

@@ -245,7 +245,7 @@ __global__ void __launch_bounds__(256, 2) cov_norm_kernel(const __nv_bfloat16* _
         if (!mbar_wait(mma_bar, 0, abort_flag, wait_ns)) {
             report(kStatusTimeout);
             *abort_flag = 1;
-            mbar_drain(mma_bar, 0);
+            mbar_drain(mma_bar, 0, abort_flag);
         }
     }
     __syncthreads();

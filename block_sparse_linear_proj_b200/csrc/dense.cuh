@@ -333,7 +333,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
         }
         if (!ok) fail();
         for (int y = 0; y < SLOTS; ++y)     // every load has landed before the CTA exits
-            if ((used >> y) & 1u) mbar_drain(&full[y], (last >> y) & 1u);
+            if ((used >> y) & 1u) mbar_drain(&full[y], (last >> y) & 1u, abort_flag);
     } else if (warp == 1 || warp == 2) {
         // ==================================================== MMA issuers (the whole warp waits, one lane issues)
         // One a stream: an issue blocks until the tensor core takes it, and a wait after it starts only then, so one
@@ -408,7 +408,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
         }
         if (!ok) fail();
         if (leader) umma_commit(o_full);   // also: every MMA has completed before tensor memory is released
-        mbar_drain(o_full, 0);
+        mbar_drain(o_full, 0, abort_flag);
     } else if (warp >= 4) {
         reg_inc<216>();
         // ==================================================== streams
@@ -1139,8 +1139,8 @@ __device__ __forceinline__ void dense_bwd_cta(const DenseBwdMaps& tm, const Dens
         }
         if (!ok) fail();
         // every load has landed before the CTA exits
-        if (KEYS && n_load > 0) mbar_drain(r_full, 0);   // (with the warps' own arrivals)
-        for (int y = max(0, i - SLOTS); y < i; ++y) mbar_drain(&full[y % SLOTS], (y / SLOTS) & 1);
+        if (KEYS && n_load > 0) mbar_drain(r_full, 0, abort_flag);   // (with the warps' own arrivals)
+        for (int y = max(0, i - SLOTS); y < i; ++y) mbar_drain(&full[y % SLOTS], (y / SLOTS) & 1, abort_flag);
     } else if (warp == 1) {
         // ==================================================== issuer of S and dP
         constexpr uint32_t ID_S = idesc_t<T>(128, 64, 0, 0);
@@ -1185,7 +1185,7 @@ __device__ __forceinline__ void dense_bwd_cta(const DenseBwdMaps& tm, const Dens
         }
         if (!ok) fail();
         if (leader) umma_commit(end_bar);      // also: every MMA has completed before tensor memory is released
-        mbar_drain(end_bar, 0);
+        mbar_drain(end_bar, 0, abort_flag);
     } else if (warp == 2) {
         // ==================================================== issuer of the accumulating products
         constexpr uint32_t ID_V = idesc_t<T>(128, D, 0, 1), ID_G = idesc_t<T>(128, 64, 0, 1);
@@ -1218,7 +1218,7 @@ __device__ __forceinline__ void dense_bwd_cta(const DenseBwdMaps& tm, const Dens
         }
         if (!ok) fail();
         if (leader) umma_commit(end_bar);
-        mbar_drain(end_bar, 0);
+        mbar_drain(end_bar, 0, abort_flag);
     } else if (warp >= 4) {
         // ==================================================== warpgroups
         const int q4 = warp & 3, w = (warp - 4) >> 2, r = q4 * 32 + lane;

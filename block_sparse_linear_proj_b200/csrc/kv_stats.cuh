@@ -412,7 +412,7 @@ __global__ void __launch_bounds__(256, 2) kv_stats_kernel(KvStatsArgs a) {
                                     __uint_as_float(v[x + 2]), __uint_as_float(v[x + 3]));
             }
         }
-        if (tid == 0 && *abort_flag && issued > 0) mbar_drain(mma_bar, (issued - 1) & 1);
+        if (tid == 0 && *abort_flag && issued > 0) mbar_drain(mma_bar, (issued - 1) & 1, abort_flag);
         tc_fence_before();
         __syncthreads();
         if (warp == 0) tmem_dealloc(tmem, TCOLS);
